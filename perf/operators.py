@@ -205,8 +205,7 @@ def prepare(case, seed):
             from bit_video_dit_b200 import nvfp4 as nv
 
             s["w"] = nv.NVFP4Tensor(s["codes"], s["scales"], a32, n, k)
-            s["out"] = torch.empty((m, -(-n // 8) * 8), dtype=torch.bfloat16, device=DEV)[:, :n]
-            s["ws"] = nv.workspace(nv.OP_GEMV, m, n, k)
+            s["out"] = torch.empty((m, n), dtype=torch.bfloat16, device=DEV)
         return s
     rows, lens = _shape(case)
     page, kv, d = case["page"], case["kv_heads"], case["d"]
@@ -274,8 +273,7 @@ def _own(s):
     from bit_video_dit_b200 import nvfp4 as nv
 
     if s["kind"] == "gemv":
-        return nv.gemv(s["x"], s["w"], out=s["out"], bias=s["bias"], act=nv.ACT_GELU_TANH if s["act"] else nv.ACT_NONE,
-                       ws=s["ws"])
+        return nv.gemv(s["x"], s["w"], out=s["out"], bias=s["bias"], act=nv.ACT_GELU_TANH if s["act"] else nv.ACT_NONE)
     cache, rows = s["cache"], s["rows"]
     if s["kind"] == "attend":
         return cache.attention(rows, s["q"], window=s["window"], sinks=s["sinks"], out=s["out"], ws=s["ws"])
