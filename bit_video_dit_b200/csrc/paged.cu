@@ -1,0 +1,762 @@
+// The paged NVFP4 cache: token rows quantized into pages as they are written,
+// read back to bf16, and attention of few rows (a decode step's) over it.  The
+// reading note's KV store (section 二 推理底座) quantizes a whole frame-chunk with
+// the chunk's own tensor scale; here a sequence grows by any number of tokens
+// a step, so the tensor scale is the cache's, given once (delayed scaling), and
+// the E4M3 block scales follow each token.
+//
+// Layout: page p, K/V head h, token o of the page: row (p * kv_heads + h) *
+// page_size + o of head_dim elements.  One head's tokens of a page are
+// contiguous, so an attention tile of one head reads whole lines.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "fp4mma.cuh"
+#include "paged.cuh"
+
+namespace nvfp4 {
+namespace paged {
+
+using namespace fp4mma;
+
+// ---------------------------------------------------------------------------
+// append and gather.  Memory bound: 2 bytes an element one way, 9/16 the other.
+// A lane holds one 16-element block, so a warp has the head_dim / 16 blocks of
+// 4 (head_dim 128) or 8 (64) consecutive rows of one head: it reads and writes
+// whole 32-byte sectors on both sides.
+// ---------------------------------------------------------------------------
+constexpr int kRowWarps = 8;
+
+struct RowArgs {
+    View v;
+    uint8_t* rows[2];  // bf16 K, V rows [n_rows][kv_heads][d]
+    int64_t ld[2];     // elements between rows
+    const float* rope_cos;  // [n_rows][d / 2] or NULL
+    const float* rope_sin;
+};
+
+// The last sequence b with row_start[b] <= row (the warp searches together,
+// 32 entries at a time).
+__device__ __forceinline__ int find_seq(const View& v, int row, int lane) {
+    int lo = 0, hi = v.n_seqs;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int64_t i = lo + (int64_t)lane * step;
+        const bool le = lane == 0 || (i < hi && __ldg(v.row_start + i) <= row);
+        lo += (__popc(__ballot_sync(0xFFFFFFFFu, le)) - 1) * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
+// 16 elements (K with RoPE when tables are given, as nvfp4_kv_append_rope) to
+// codes and scale at cache row `at`, block `blk`.
+__device__ __forceinline__ void append_block(const RowArgs& a, int t, int row, int head, int blk, int64_t at) {
+    const View& v = a.v;
+    const uint8_t* src = a.rows[t] + ((int64_t)row * a.ld[t] + (int64_t)head * v.d + 16 * blk) * 2;
+    float x[16];
+    bf16x8_to_f32(ld_stream16(src), x);
+    bf16x8_to_f32(ld_stream16(src + 16), x + 8);
+    if (t == 0 && a.rope_cos) {
+        const int64_t off = (int64_t)row * (v.d / 2) + 8 * blk;
+        const float4* pc = reinterpret_cast<const float4*>(a.rope_cos + off);
+        const float4* ps = reinterpret_cast<const float4*>(a.rope_sin + off);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const float4 c4 = __ldg(pc + i), s4 = __ldg(ps + i);
+            const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                float &x0 = x[8 * i + 2 * e], &x1 = x[8 * i + 2 * e + 1];
+                const float y0 = __fsub_rn(__fmul_rn(x0, c[e]), __fmul_rn(x1, s[e]));
+                x1 = __fadd_rn(__fmul_rn(x0, s[e]), __fmul_rn(x1, c[e]));
+                x0 = y0;
+            }
+        }
+    }
+    const BlockScale b = block_scale(fmaxf(absmax8(x), absmax8(x + 8)), __ldg(v.a32[t]));
+    uint8_t* codes = const_cast<uint8_t*>(v.codes[t]) + at * (v.d / 2) + 8 * blk;
+    *reinterpret_cast<uint2*>(codes) = make_uint2(encode8(x, b.inv), encode8(x + 8, b.inv));
+    const_cast<uint8_t*>(v.scales[t])[at * (v.d / 16) + blk] = (uint8_t)b.code;
+}
+
+__device__ __forceinline__ void gather_block(const RowArgs& a, int t, int row, int head, int blk, int64_t at) {
+    const View& v = a.v;
+    uint32_t o[8];
+    if (at >= 0) {
+        const uint2 c = __ldg(reinterpret_cast<const uint2*>(v.codes[t] + at * (v.d / 2) + 8 * blk));
+        const uint32_t sc = __ldg(v.scales[t] + at * (v.d / 16) + blk);
+        const __half2 s2 = e4m3x2_to_half2((uint16_t)(sc | (sc << 8)));
+        const float a32 = __ldg(v.a32[t]);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float2 f =
+                __half22float2(__hmul2(e2m1x2_to_half2(((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu), s2));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(f.x, a32), __fmul_rn(f.y, a32));
+            o[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) o[i] = 0u;
+    }
+    uint4* dst = reinterpret_cast<uint4*>(a.rows[t] + ((int64_t)row * a.ld[t] + (int64_t)head * v.d + 16 * blk) * 2);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <bool APPEND>
+__global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_constant__ RowArgs a) {
+    const View& v = a.v;
+    const int lane = threadIdx.x & 31;
+    const int blocks = v.d / 16, per = 32 / blocks;  // lanes of a row, rows of a warp
+    int64_t w = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    const int t = (int)(w & 1);
+    w >>= 1;
+    const int head = (int)(w % v.kv_heads);
+    const int64_t r0 = w / v.kv_heads * per;
+    if (r0 >= v.n_rows) return;
+    const int last = (int)min((int64_t)v.n_rows, r0 + per) - 1;
+    int b = find_seq(v, (int)r0, lane);
+    const int b1 = find_seq(v, last, lane);
+    const int row = (int)r0 + lane / blocks, blk = lane % blocks;
+    if (row > last) return;
+    if (b != b1) {  // the rows' own sequences lie between
+        int lo = b, hi = b1 + 1;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (__ldg(v.row_start + mid) <= row) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+    }
+    const Seq s = load_seq(v, b);
+    if (row < s.first || row - s.first >= s.n) return;  // no sequence's row: left as it was
+    const int pos = s.len - s.n + (row - s.first);
+    if (pos < 0) {  // before the sequence's first position
+        if (!APPEND) gather_block(a, t, row, head, blk, -1);
+        return;
+    }
+    const int page = page_of(v, b, pos);
+    if (page < 0) return;
+    const int64_t at = cache_row(v, page, head, pos);
+    if (APPEND) append_block(a, t, row, head, blk, at);
+    else gather_block(a, t, row, head, blk, at);
+}
+
+// ---------------------------------------------------------------------------
+// attention of few rows.
+//
+// Unit: one sequence, one K/V head, up to 8 NT rows (row, query head of the
+// group) and a run of 32-key tiles; 4 warps take the tiles in turn, each with
+// its own running maximum and sum.  Both products have the cache as the A
+// operand (S^T = K Q^T, O^T = V^T P^T), so eight rows fill a matrix
+// instruction's columns; a lane's loads are whole 16-byte (K) and 8-byte (V)
+// pieces of rows, with the contraction's columns permuted to fit, and P^T comes
+// from S^T by an 8 x 8 transpose in registers.
+//
+// Bound: the cache's bytes (a key and value are 9/8 head_dim bytes a head),
+// and beside them the decoding (fp4mma.cuh).  Long sequences are split over
+// CTAs and joined by combine_kernel.
+// ---------------------------------------------------------------------------
+constexpr int kKeys = 32;  // keys of a tile
+constexpr int kWarps = 4;
+constexpr float kLazy = 8.0f;      // a reference maximum moves when exceeded by more than 2^8
+constexpr float kFloor = -1e30f;   // the reference before any visible key
+
+struct AttnArgs {
+    View v;
+    const uint8_t* q;  // bf16 [n_rows][heads][d], ld_q elements between rows
+    uint8_t* o;
+    int64_t ld_q, ld_o;
+    int heads, group, window, sinks, max_rows;
+    int row_tiles, splits, split_tiles;
+    float scale_log2;
+    float* part_o;   // [splits][n_rows][heads][d]
+    float2* part_ml; // [splits][n_rows][heads] (reference maximum, sum)
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Rows f0 .. f0 + cols - 1 of a sequence's n * group (row, query head) pairs.
+struct Rows {
+    int n;     // pairs in the unit
+    Span span;
+};
+
+__device__ __forceinline__ Rows unit_rows(const AttnArgs& a, const Seq& s, int f0, int cols) {
+    Rows r;
+    r.n = min(cols, s.n * a.group - f0);
+    if (r.n <= 0) {
+        r.n = 0;
+        r.span = Span{0, 0, 0};
+        return r;
+    }
+    const int p = s.len - s.n;
+    r.span = visible_span(p + f0 / a.group, p + (f0 + r.n - 1) / a.group, a.window, a.sinks);
+    return r;
+}
+
+// Tiles of one split of a unit with `count` tiles.
+__device__ __forceinline__ int tiles_per_split(const AttnArgs& a, int count) {
+    return max(a.split_tiles, (count + a.splits - 1) / a.splits);
+}
+
+template <int D>
+struct KVTile {
+    uint4 k[2][2];     // keys 16 q + g, + 8: 8 * D / 32 codes from D / 4 * t (D = 64: .x, .y)
+    uint32_t ks[2];    // their scales: key g in bits 15:0, key g + 8 in 31:16
+    uint2 v[2][4];     // keys 16 q + 2 t + {0, 1, 8, 9}: D / 8 codes from D / 8 * g (D = 64: .x)
+    uint32_t vs[2];    // their scales, one a byte
+    bool ok[2];        // the 16 keys lie in a page of the cache
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(const View& v, int b, int head, const Span& sp, int k0, int g, int t,
+                                          KVTile<D>& x) {
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+        const int kq = k0 + 16 * q;
+        const int page = group_seen(sp, kq) ? page_of(v, b, kq) : -1;
+        x.ok[q] = page >= 0;
+        if (page >= 0) {
+            const int64_t r = cache_row(v, page, head, kq);
+            const uint8_t* kc = v.codes[0] + r * (D / 2) + D / 8 * t;
+            const uint8_t* vc = v.codes[1] + (r + 2 * t) * (D / 2) + D / 16 * g;
+            const uint8_t* ks = v.scales[0] + r * (D / 16);
+            const uint8_t* vs = v.scales[1] + (r + 2 * t) * (D / 16) + (D == 128 ? g : g / 2);
+            if (D == 128) {
+                x.k[q][0] = ld_stream16(kc + g * 64);
+                x.k[q][1] = ld_stream16(kc + (g + 8) * 64);
+                x.ks[q] = __ldg(reinterpret_cast<const uint16_t*>(ks + g * 8 + 2 * t)) |
+                          ((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(ks + (g + 8) * 8 + 2 * t)) << 16);
+            } else {
+                const uint2 k0v = __ldg(reinterpret_cast<const uint2*>(kc + g * 32));
+                const uint2 k1v = __ldg(reinterpret_cast<const uint2*>(kc + (g + 8) * 32));
+                x.k[q][0] = make_uint4(k0v.x, k0v.y, 0u, 0u);
+                x.k[q][1] = make_uint4(k1v.x, k1v.y, 0u, 0u);
+                const uint32_t s0 = __ldg(ks + g * 4 + t), s1 = __ldg(ks + (g + 8) * 4 + t);
+                x.ks[q] = (s0 | (s0 << 8)) | ((s1 | (s1 << 8)) << 16);
+            }
+            uint32_t s4 = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int key = (i & 1) + 8 * (i >> 1);  // + 2 t
+                const bool in = kq + 2 * t + key < sp.hi;  // what lies behind the last key is not a value
+                if (D == 128)
+                    x.v[q][i] = in ? __ldg(reinterpret_cast<const uint2*>(vc + key * 64)) : make_uint2(0u, 0u);
+                else
+                    x.v[q][i] = make_uint2(in ? __ldg(reinterpret_cast<const uint32_t*>(vc + key * 32)) : 0u, 0u);
+                s4 |= (in ? (uint32_t)__ldg(vs + key * (D / 16)) : 0u) << (8 * i);
+            }
+            x.vs[q] = s4;
+        } else {
+            x.k[q][0] = x.k[q][1] = make_uint4(0u, 0u, 0u, 0u);
+            x.ks[q] = x.vs[q] = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; i++) x.v[q][i] = make_uint2(0u, 0u);
+        }
+    }
+}
+
+// One key row's D / 4 codes and its scales (bits 15:0: two blocks, or one twice) -> D / 8 pairs
+template <int D>
+__device__ __forceinline__ void decode_k(const uint4& c, uint32_t sc, uint32_t* o) {
+    const __half2 s = __hmul2(e4m3x2_to_half2((uint16_t)sc), bits_h2((kMulBits << 16) | (kMulCvt & 0xFFFFu)));
+    const __half2 s0 = __low2half2(s), s1 = __high2half2(s);
+    if (D == 128) {
+        decode8_cvt(c.x, s0, o);
+        decode8_cvt(c.y, s0, o + 4);
+        decode8_bits(c.z, s1, o + 8);
+        decode8_bits(c.w, s1, o + 12);
+    } else {
+        decode8_cvt(c.x, s0, o);
+        decode8_bits(c.y, s1, o + 4);
+    }
+}
+
+// The same 8 codes of keys a and b -> pairs (a_i, b_i), i = 0..7.
+__device__ __forceinline__ void decode_v_bits(uint32_t wa, uint32_t wb, __half2 s, uint32_t* o) {
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const uint32_t x = __byte_perm(wa, wb, h ? 0x7632 : 0x5410);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t y = x << (12 - 4 * i);
+            o[4 * h + i] = h2_bits(__hmul2(bits_h2((y & 0x80008000u) | ((y >> 3) & 0x0E000E00u)), s));
+        }
+    }
+}
+__device__ __forceinline__ void decode_v_cvt(uint32_t wa, uint32_t wb, __half2 s, uint32_t* o) {
+    const uint32_t e = (wa & 0x0F0F0F0Fu) | ((wb << 4) & 0xF0F0F0F0u);
+    const uint32_t d = ((wa >> 4) & 0x0F0F0F0Fu) | (wb & 0xF0F0F0F0u);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        o[2 * i] = h2_bits(__hmul2(e2m1x2_to_half2((e >> (8 * i)) & 0xFFu), s));
+        o[2 * i + 1] = h2_bits(__hmul2(e2m1x2_to_half2((d >> (8 * i)) & 0xFFu), s));
+    }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32) decode_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int kCols = 8 * NT, kSteps = D / 16, kPer = D / 8;  // kPer: a lane's channels of O
+    __shared__ float so[kWarps][kCols][D + 4];
+    __shared__ float2 sml[kWarps][kCols];
+    const View& v = a.v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    unsigned u = blockIdx.x;
+    const int split = (int)(u % (unsigned)a.splits);
+    u /= (unsigned)a.splits;
+    const int rt = (int)(u % (unsigned)a.row_tiles);
+    u /= (unsigned)a.row_tiles;
+    const int head = (int)(u % (unsigned)v.kv_heads), b = (int)(u / (unsigned)v.kv_heads);
+    const Seq s = load_seq(v, b);
+    if (s.n > a.max_rows) {  // more rows than the launch was sized for
+        record_error(v.err, NVFP4_ERR_DEVICE, (uint32_t)b);
+        return;
+    }
+    const int f0 = rt * kCols;
+    const Rows rows = unit_rows(a, s, f0, kCols);
+    if (rows.n == 0) return;
+    const Tiles<kKeys> tiles(rows.span);
+    const int per = tiles_per_split(a, tiles.count);
+    const int begin = split * per, end = min(tiles.count, begin + per);
+    if (a.splits > 1 && begin >= end && split > 0) return;
+
+    // queries: column n of tile j is row f0 + 8 j + n
+    uint32_t qb[NT][D / 8];
+    float c_col[NT][2];
+    int lo_col[NT][2], hi_col[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+        uint4 raw[D / 32];
+        const int f = f0 + 8 * j + g;
+        const bool in = 8 * j + g < rows.n;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((int64_t)(s.first + f / a.group) * a.ld_q + (int64_t)(head * a.group + f % a.group) * D + D / 4 * t) * 2);
+#pragma unroll
+        for (int i = 0; i < D / 32; i++) raw[i] = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        const float back = scale_row<D / 32>(raw, qb[j]);
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            c_col[j][e] = __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4 * e) * (__ldg(v.a32[0]) * a.scale_log2 * kDecodeBack);
+            const int n = 8 * j + 2 * t + e;
+            const int p = s.len - s.n + (f0 + n) / a.group;
+            hi_col[j][e] = n < rows.n ? p + 1 : 0;
+            lo_col[j][e] = a.window > 0 ? p - a.window + 1 : 0;
+        }
+    }
+    const int p_first = s.len - s.n + f0 / a.group;  // the unit's first and last positions
+    const int p_last = s.len - s.n + (f0 + rows.n - 1) / a.group;
+
+    float m[NT][2], l[NT][2], o[NT][kSteps][4];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            m[j][e] = kFloor;
+            l[j][e] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[j][i][e] = 0.0f;
+    }
+
+    KVTile<D> x;
+    if (begin + warp < end) load_tile<D>(v, b, head, rows.span, tiles.key0(begin + warp), g, t, x);
+    for (int i = begin + warp; i < end; i += kWarps) {
+        const int k0 = tiles.key0(i);
+        KVTile<D> next;
+        if (i + kWarps < end) load_tile<D>(v, b, head, rows.span, tiles.key0(i + kWarps), g, t, next);
+        float z[2][NT][4];
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            uint32_t ka[D / 8], kb[D / 8];
+            decode_k<D>(x.k[q][0], x.ks[q] & 0xFFFFu, ka);
+            decode_k<D>(x.k[q][1], x.ks[q] >> 16, kb);
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) z[q][j][e] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < kSteps; e++)
+                    mma_16816(z[q][j], ka[2 * e], kb[2 * e], ka[2 * e + 1], kb[2 * e + 1], qb[j][2 * e], qb[j][2 * e + 1]);
+#pragma unroll
+                for (int e = 0; e < 4; e++) z[q][j][e] *= c_col[j][e & 1];
+            }
+        }
+        // every key of the tile seen by every row, or else key by key
+        const bool all = x.ok[0] && x.ok[1] && k0 + kKeys - 1 <= p_first &&
+                         (a.window == 0 || k0 > p_last - a.window || k0 + kKeys <= a.sinks);
+        if (!all || rows.n < kCols) {
+#pragma unroll
+            for (int q = 0; q < 2; q++)
+#pragma unroll
+                for (int j = 0; j < NT; j++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int key = k0 + 16 * q + g + 8 * (e >> 1);
+                        const bool seen = x.ok[q] && key < hi_col[j][e & 1] && (key >= lo_col[j][e & 1] || key < a.sinks);
+                        if (!seen) z[q][j][e] = -INFINITY;
+                    }
+        }
+        bool over = false;
+#pragma unroll
+        for (int q = 0; q < 2; q++)
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) over |= z[q][j][e] > m[j][e & 1] + kLazy;
+        if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float mx = fmaxf(fmaxf(z[0][j][e], z[0][j][e + 2]), fmaxf(z[1][j][e], z[1][j][e + 2]));
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+                    if (mx > m[j][e] + kLazy) {
+                        const float f = ex2(m[j][e] - mx);
+                        m[j][e] = mx;
+                        l[j][e] *= f;
+#pragma unroll
+                        for (int r = 0; r < kSteps; r++) {
+                            o[j][r][e] *= f;
+                            o[j][r][e + 2] *= f;
+                        }
+                    }
+                }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    p[e] = ex2(z[q][j][e] - m[j][e & 1]);
+                    l[j][e & 1] += p[e];
+                }
+                // the weights go to the tensor cores in binary16 (2^-11 of each)
+                pb[j][0] = transpose8x8(h2_bits(__floats2half2_rn(p[0], p[1])));
+                pb[j][1] = transpose8x8(h2_bits(__floats2half2_rn(p[2], p[3])));
+            }
+            // V: channels kPer g + 0 .. kPer - 1 of the lane's four keys, two keys a pair
+            uint32_t va[kPer], vb[kPer];
+            const __half2 s01 = e4m3x2_to_half2((uint16_t)(x.vs[q] & 0xFFFFu));
+            const __half2 s23 = e4m3x2_to_half2((uint16_t)(x.vs[q] >> 16));
+            const __half2 by6 = bits_h2(kMulBits), by8 = bits_h2(kMulCvt);
+            decode_v_bits(x.v[q][0].x, x.v[q][1].x, __hmul2(s01, by6), va);
+            decode_v_bits(x.v[q][2].x, x.v[q][3].x, __hmul2(s23, by6), vb);
+            if (D == 128) {
+                decode_v_cvt(x.v[q][0].y, x.v[q][1].y, __hmul2(s01, by8), va + 8);
+                decode_v_cvt(x.v[q][2].y, x.v[q][3].y, __hmul2(s23, by8), vb + 8);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+#pragma unroll
+                for (int r = 0; r < kSteps; r++)
+                    mma_16816(o[j][r], va[2 * r], va[2 * r + 1], vb[2 * r], vb[2 * r + 1], pb[j][0], pb[j][1]);
+        }
+        x = next;
+    }
+
+    // join the four warps
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            float sum = l[j][e];
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+            if (g == 0) sml[warp][8 * j + 2 * t + e] = make_float2(m[j][e], sum);
+#pragma unroll
+            for (int r = 0; r < kSteps; r++) {
+                so[warp][8 * j + 2 * t + e][kPer * g + 2 * r] = o[j][r][e];
+                so[warp][8 * j + 2 * t + e][kPer * g + 2 * r + 1] = o[j][r][e + 2];
+            }
+        }
+    __syncthreads();
+    const float back = __ldg(v.a32[1]) * kDecodeBack;
+    for (int i = threadIdx.x; i < rows.n * (D / 2); i += kWarps * 32) {
+        const int n = i / (D / 2), d = i % (D / 2) * 2;
+        float mx = sml[0][n].x;
+#pragma unroll
+        for (int w = 1; w < kWarps; w++) mx = fmaxf(mx, sml[w][n].x);
+        float sum = 0.0f, y0 = 0.0f, y1 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            const float f = ex2(sml[w][n].x - mx);
+            sum += sml[w][n].y * f;
+            y0 += so[w][n][d] * f;
+            y1 += so[w][n][d + 1] * f;
+        }
+        const int row = s.first + (f0 + n) / a.group, qh = head * a.group + (f0 + n) % a.group;
+        if (a.splits > 1) {
+            const int64_t slot = ((int64_t)split * v.n_rows + row) * a.heads + qh;
+            *reinterpret_cast<float2*>(a.part_o + slot * D + d) = make_float2(y0, y1);
+            if (d == 0) a.part_ml[slot] = make_float2(mx, sum);
+        } else {
+            const float f = sum > 0.0f ? __fdiv_rn(back, sum) : 0.0f;  // a row that sees no key: zeros
+            *reinterpret_cast<__nv_bfloat162*>(a.o + ((int64_t)row * a.ld_o + (int64_t)qh * D + d) * 2) =
+                __floats2bfloat162_rn(y0 * f, y1 * f);
+        }
+    }
+}
+
+// A warp joins the splits of one (row, query head).  `cols` and T: the rows of
+// a unit and the keys of a tile in the kernel that wrote the parts.
+template <int D, int T>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ AttnArgs a, int cols) {
+    const View& v = a.v;
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const int64_t each = (int64_t)a.max_rows * a.heads;
+    const int b = (int)(w / each), i = (int)(w % each) / a.heads, qh = (int)(w % each) % a.heads;
+    if (b >= v.n_seqs) return;
+    const Seq s = load_seq(v, b);
+    if (s.n > a.max_rows || i >= s.n) return;
+    const int f = i * a.group + qh % a.group;
+    const Rows rows = unit_rows(a, s, f / cols * cols, cols);
+    const Tiles<T> tiles(rows.span);
+    const int per = tiles_per_split(a, tiles.count);
+    const int parts = max(1, (tiles.count + per - 1) / per);
+    const int64_t row = s.first + i;
+    float mx = kFloor, sum = 0.0f, y[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; e++) y[e] = 0.0f;
+    for (int p = 0; p < parts; p++) mx = fmaxf(mx, __ldcg(&a.part_ml[((int64_t)p * v.n_rows + row) * a.heads + qh].x));
+    for (int p = 0; p < parts; p++) {
+        const int64_t slot = ((int64_t)p * v.n_rows + row) * a.heads + qh;
+        const float2 ml = __ldcg(a.part_ml + slot);
+        const float wgt = ex2(ml.x - mx);
+        sum += ml.y * wgt;
+#pragma unroll
+        for (int e = 0; e < D / 64; e++) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(a.part_o + slot * D) + 32 * e + lane);
+            y[2 * e] += x.x * wgt;
+            y[2 * e + 1] += x.y * wgt;
+        }
+    }
+    const float f2 = sum > 0.0f ? __fdiv_rn(__ldg(v.a32[1]) * kDecodeBack, sum) : 0.0f;
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + (row * a.ld_o + (int64_t)qh * D) * 2);
+#pragma unroll
+    for (int e = 0; e < D / 64; e++) dst[32 * e + lane] = __floats2bfloat162_rn(y[2 * e] * f2, y[2 * e + 1] * f2);
+}
+
+}  // namespace paged
+}  // namespace nvfp4
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+using namespace nvfp4;
+using namespace nvfp4::paged;
+
+namespace {
+
+constexpr int kSms = 148;
+constexpr size_t kControl = 256;
+
+bool odd(const void* p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
+
+// The checks of the cache and the rows that all three calls share.
+nvfp4_status check_paged(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, const void* ws, size_t ws_bytes,
+                         size_t need) {
+    if (!c || !r || !ws || ws_bytes < need) return NVFP4_ERR_INVALID_ARG;
+    if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales || !c->k_global || !c->v_global || c->n_pages <= 0 ||
+        c->page_size <= 0 || c->kv_heads <= 0)
+        return NVFP4_ERR_INVALID_ARG;
+    if (r->n_seqs < 0 || r->n_rows < 0 || r->max_pages < 0 || r->max_rows < 0 || r->max_len < 0)
+        return NVFP4_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return NVFP4_ERR_UNSUPPORTED;
+    if (c->page_size % kGroup != 0 || c->page_size > (1 << 20) || c->kv_heads > (1 << 16) || r->n_rows > (1 << 30) ||
+        r->max_len > (1 << 30))
+        return NVFP4_ERR_UNSUPPORTED;
+    if (r->n_seqs > 0 && r->n_rows > 0 && (!r->row_start || !r->lens || (r->max_pages > 0 && !r->pages)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (odd(c->k_codes, 15u) || odd(c->k_scales, 15u) || odd(c->v_codes, 15u) || odd(c->v_scales, 15u) ||
+        odd(c->k_global, 3u) || odd(c->v_global, 3u) || odd(r->row_start, 3u) || odd(r->lens, 3u) || odd(r->pages, 3u) ||
+        odd(ws, 255u))
+        return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+View make_view(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, void* ws) {
+    View v{};
+    v.codes[0] = static_cast<const uint8_t*>(c->k_codes);
+    v.codes[1] = static_cast<const uint8_t*>(c->v_codes);
+    v.scales[0] = static_cast<const uint8_t*>(c->k_scales);
+    v.scales[1] = static_cast<const uint8_t*>(c->v_scales);
+    v.a32[0] = c->k_global;
+    v.a32[1] = c->v_global;
+    v.row_start = r->row_start;
+    v.lens = r->lens;
+    v.pages = r->pages;
+    v.n_pages = c->n_pages;
+    v.page_size = c->page_size;
+    v.kv_heads = c->kv_heads;
+    v.d = c->head_dim;
+    v.n_seqs = r->n_seqs;
+    v.max_pages = r->max_pages;
+    v.n_rows = r->n_rows;
+    v.err = static_cast<DevError*>(ws);
+    return v;
+}
+
+nvfp4_status rows_call(bool append, const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, const void* k, int64_t ld_k,
+                       const void* v, int64_t ld_v, const float* rope_cos, const float* rope_sin, void* ws,
+                       size_t ws_bytes, nvfp4_stream_t stream) {
+    const nvfp4_status st = check_paged(c, r, ws, ws_bytes, kControl);
+    if (st != NVFP4_OK) return st;
+    const int64_t width = (int64_t)c->kv_heads * c->head_dim;
+    if (ld_k < width || ld_v < width || (rope_cos == nullptr) != (rope_sin == nullptr)) return NVFP4_ERR_INVALID_ARG;
+    if (r->n_rows == 0 || r->n_seqs == 0) return NVFP4_OK;
+    if (!k || !v) return NVFP4_ERR_INVALID_ARG;
+    if (odd(k, 15u) || odd(v, 15u) || ld_k % 8 != 0 || ld_v % 8 != 0 || odd(rope_cos, 15u) || odd(rope_sin, 15u))
+        return NVFP4_ERR_MISALIGNED;
+    RowArgs a{};
+    a.v = make_view(c, r, ws);
+    a.rows[0] = static_cast<uint8_t*>(const_cast<void*>(k));
+    a.rows[1] = static_cast<uint8_t*>(const_cast<void*>(v));
+    a.ld[0] = ld_k;
+    a.ld[1] = ld_v;
+    a.rope_cos = rope_cos;
+    a.rope_sin = rope_sin;
+    const int64_t per = 512 / c->head_dim;  // rows of a warp
+    const int64_t warps = (r->n_rows + per - 1) / per * c->kv_heads * 2;
+    const int64_t grid = (warps + kRowWarps - 1) / kRowWarps;
+    if (grid >= ((int64_t)1 << 31)) return NVFP4_ERR_UNSUPPORTED;
+    if (append) rows_kernel<true><<<(unsigned)grid, kRowWarps * 32, 0, (cudaStream_t)stream>>>(a);
+    else rows_kernel<false><<<(unsigned)grid, kRowWarps * 32, 0, (cudaStream_t)stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+// How an attention call is cut up; the same for its workspace query.
+struct Plan {
+    int cols;  // (row, query head) pairs of a unit
+    int row_tiles, splits, split_tiles;
+    int64_t units;
+    size_t ws;
+};
+
+bool make_plan(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, int heads, int window, int sinks, Plan* p) {
+    const int64_t pairs = (int64_t)r->max_rows * (heads / c->kv_heads);
+    if (pairs >= ((int64_t)1 << 31)) return false;
+    p->cols = pairs <= 8 ? 8 : 16;
+    const int64_t row_tiles = std::max<int64_t>(1, (pairs + p->cols - 1) / p->cols);
+    p->units = row_tiles * c->kv_heads * std::max(1, r->n_seqs);
+    if (p->units >= ((int64_t)1 << 31)) return false;
+    p->row_tiles = (int)row_tiles;
+    // the most tiles that one unit can see
+    const int64_t unit_rows = std::min<int64_t>(r->max_rows, p->cols);
+    int64_t seen = r->max_len;
+    if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + unit_rows + sinks + 2 * kKeys);
+    const int64_t most = (seen + kKeys - 1) / kKeys;
+    // runs of tiles such that about eight CTAs an SM have work, none shorter than a tile a warp
+    const int64_t want = std::max<int64_t>(1, (int64_t)kSms * 8 / p->units);
+    int64_t per = std::max<int64_t>(kWarps, (most + want - 1) / want);
+    int64_t splits = std::max<int64_t>(1, (most + per - 1) / per);
+    if (p->units * splits >= ((int64_t)1 << 31)) return false;
+    p->splits = (int)splits;
+    p->split_tiles = (int)per;
+    p->ws = kControl;
+    if (splits > 1) {
+        const int64_t slots = splits * (int64_t)r->n_rows * heads;
+        p->ws += (size_t)(slots * c->head_dim * 4 + slots * 8);
+    }
+    return true;
+}
+
+nvfp4_status check_heads(const nvfp4_paged_cache* c, int heads, int window, int sinks) {
+    if (heads <= 0 || heads % c->kv_heads != 0 || window < 0 || sinks < 0) return NVFP4_ERR_INVALID_ARG;
+    if (heads > (1 << 16) || window > (1 << 30) || sinks > (1 << 30)) return NVFP4_ERR_UNSUPPORTED;
+    return NVFP4_OK;
+}
+
+}  // namespace
+
+extern "C" nvfp4_status nvfp4_paged_append(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows,
+                                           const void* k_bf16, int64_t ld_k, const void* v_bf16, int64_t ld_v,
+                                           const float* rope_cos, const float* rope_sin, void* workspace,
+                                           size_t ws_bytes, nvfp4_stream_t stream) {
+    return rows_call(true, cache, rows, k_bf16, ld_k, v_bf16, ld_v, rope_cos, rope_sin, workspace, ws_bytes, stream);
+}
+
+extern "C" nvfp4_status nvfp4_paged_gather(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows, void* k_bf16,
+                                           int64_t ld_k, void* v_bf16, int64_t ld_v, void* workspace, size_t ws_bytes,
+                                           nvfp4_stream_t stream) {
+    return rows_call(false, cache, rows, k_bf16, ld_k, v_bf16, ld_v, nullptr, nullptr, workspace, ws_bytes, stream);
+}
+
+extern "C" size_t nvfp4_paged_attention_workspace_bytes(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows,
+                                                        int32_t heads, int32_t window, int32_t sinks) {
+    Plan p;
+    if (!cache || !rows || cache->kv_heads <= 0 || (cache->head_dim != 64 && cache->head_dim != 128) ||
+        rows->n_seqs < 0 || rows->n_rows < 0 || rows->max_rows < 0 || rows->max_len < 0 ||
+        check_heads(cache, heads, window, sinks) != NVFP4_OK || !make_plan(cache, rows, heads, window, sinks, &p))
+        return 0;
+    return p.ws;
+}
+
+extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows,
+                                              const void* q_bf16, int64_t ld_q, int32_t heads, int32_t window,
+                                              int32_t sinks, float scale, void* o_bf16, int64_t ld_o, void* workspace,
+                                              size_t ws_bytes, nvfp4_stream_t stream) {
+    nvfp4_status st = check_paged(cache, rows, workspace, ws_bytes, kControl);
+    if (st != NVFP4_OK) return st;
+    st = check_heads(cache, heads, window, sinks);
+    if (st != NVFP4_OK) return st;
+    const int64_t width = (int64_t)heads * cache->head_dim;
+    if (!(scale >= 0.0f) || std::isinf(scale) || ld_q < width || ld_o < width) return NVFP4_ERR_INVALID_ARG;
+    Plan p;
+    if (!make_plan(cache, rows, heads, window, sinks, &p)) return NVFP4_ERR_UNSUPPORTED;
+    if (ws_bytes < p.ws) return NVFP4_ERR_INVALID_ARG;
+    if (rows->n_rows == 0 || rows->n_seqs == 0 || rows->max_rows == 0) return NVFP4_OK;
+    if (!q_bf16 || !o_bf16) return NVFP4_ERR_INVALID_ARG;
+    if (odd(q_bf16, 15u) || odd(o_bf16, 15u) || ld_q % 8 != 0 || ld_o % 8 != 0) return NVFP4_ERR_MISALIGNED;
+    AttnArgs a{};
+    a.v = make_view(cache, rows, workspace);
+    a.q = static_cast<const uint8_t*>(q_bf16);
+    a.o = static_cast<uint8_t*>(o_bf16);
+    a.ld_q = ld_q;
+    a.ld_o = ld_o;
+    a.heads = heads;
+    a.group = heads / cache->kv_heads;
+    a.window = window;
+    a.sinks = window > 0 ? sinks : 0;
+    a.max_rows = rows->max_rows;
+    a.row_tiles = p.row_tiles;
+    a.splits = p.splits;
+    a.split_tiles = p.split_tiles;
+    const float sc = scale > 0.0f ? scale : 1.0f / sqrtf((float)cache->head_dim);
+    a.scale_log2 = sc * 1.4426950408889634f;  // log2(e)
+    const int64_t slots = (int64_t)p.splits * rows->n_rows * heads;
+    a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kControl);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * cache->head_dim);
+    void (*kern)(AttnArgs) = cache->head_dim == 128 ? (p.cols == 8 ? decode_kernel<128, 1> : decode_kernel<128, 2>)
+                                                    : (p.cols == 8 ? decode_kernel<64, 1> : decode_kernel<64, 2>);
+    kern<<<(unsigned)(p.units * p.splits), kWarps * 32, 0, (cudaStream_t)stream>>>(a);
+    if (p.splits > 1) {
+        const int64_t warps = (int64_t)rows->n_seqs * rows->max_rows * heads;
+        const int64_t grid = (warps + 3) / 4;
+        if (grid >= ((int64_t)1 << 31)) return NVFP4_ERR_UNSUPPORTED;
+        if (cache->head_dim == 128)
+            combine_kernel<128, kKeys><<<(unsigned)grid, 128, 0, (cudaStream_t)stream>>>(a, p.cols);
+        else
+            combine_kernel<64, kKeys><<<(unsigned)grid, 128, 0, (cudaStream_t)stream>>>(a, p.cols);
+    }
+    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}

@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_PKG, "libnvfp4.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE = range(7)
 (OP_QUANTIZE, OP_GEMM, OP_KV_APPEND, OP_KV_DEQUANT, OP_LN_QUANTIZE, OP_QUANTIZE_2D, OP_QUANTIZE_T,
- OP_KV_ATTENTION) = range(8)
+ OP_KV_ATTENTION, OP_PAGED_ROWS) = range(9)
 Q_COMPUTE_GLOBAL, Q_GIVEN_GLOBAL, Q_ROWMAJOR_SCALES, Q_SCALE_SEARCH = 0, 1, 2, 4
 KV_SCALE_SEARCH, KV_SMOOTH_K, KV_SMOOTH_V = 1, 2, 4
 ACT_NONE, ACT_GELU_TANH = 0, 1
@@ -28,7 +28,8 @@ EXPORTS = ("nvfp4_status_string", "nvfp4_version", "nvfp4_codes_bytes", "nvfp4_s
            "nvfp4_workspace_bytes", "nvfp4_read_device_error", "nvfp4_quantize", "nvfp4_gemm",
            "nvfp4_kv_append", "nvfp4_kv_dequant", "nvfp4_test_encode", "nvfp4_quantize_noalloc",
            "nvfp4_ln_modulate_quantize", "nvfp4_quantize_2d", "nvfp4_quantize_t", "nvfp4_attention_chunks",
-           "nvfp4_kv_attention", "nvfp4_kv_append_rope")
+           "nvfp4_kv_attention", "nvfp4_kv_append_rope", "nvfp4_gemv", "nvfp4_paged_append", "nvfp4_paged_gather",
+           "nvfp4_paged_attention", "nvfp4_paged_attention_workspace_bytes")
 
 
 class NVFP4Error(RuntimeError):
@@ -57,6 +58,19 @@ class CKVCache(ctypes.Structure):
                 ("n_slots", ctypes.c_int32), ("tokens_per_slot", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("flags", ctypes.c_uint32), ("k_mean", ctypes.c_void_p),
                 ("v_mean", ctypes.c_void_p)]
+
+
+class CPagedCache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_global", ctypes.c_void_p), ("v_global", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class CPagedRows(ctypes.Structure):
+    _fields_ = [("row_start", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("max_len", ctypes.c_int32)]
 
 
 _lib = None
@@ -108,6 +122,17 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_attention_chunks.restype = i32
         L.nvfp4_kv_attention.argtypes = [ctypes.POINTER(CKVCache), vp, i32, vp, i32, ctypes.c_float, vp, vp, sz, vp]
         L.nvfp4_kv_attention.restype = st
+        L.nvfp4_gemv.argtypes = [vp, i64, i64, ctypes.POINTER(CTensor), vp, i64, ctypes.POINTER(CEpilogue), vp]
+        L.nvfp4_gemv.restype = st
+        pc, pr = ctypes.POINTER(CPagedCache), ctypes.POINTER(CPagedRows)
+        L.nvfp4_paged_append.argtypes = [pc, pr, vp, i64, vp, i64, vp, vp, vp, sz, vp]
+        L.nvfp4_paged_append.restype = st
+        L.nvfp4_paged_gather.argtypes = [pc, pr, vp, i64, vp, i64, vp, sz, vp]
+        L.nvfp4_paged_gather.restype = st
+        L.nvfp4_paged_attention.argtypes = [pc, pr, vp, i64, i32, i32, i32, ctypes.c_float, vp, i64, vp, sz, vp]
+        L.nvfp4_paged_attention.restype = st
+        L.nvfp4_paged_attention_workspace_bytes.argtypes = [pc, pr, i32, i32, i32]
+        L.nvfp4_paged_attention_workspace_bytes.restype = sz
         _lib = L
     return _lib
 
@@ -328,6 +353,55 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, *, out: torch.Tensor | None = None, bia
     return out
 
 
+def _launch_on(device: torch.device, stream, fn, *args) -> int:
+    """Call fn(*args, stream) with `device` current (its current stream when none is given)."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(stream))
+
+
+def _same_device(device: torch.device, *ts) -> None:
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError(f"every tensor of the call has to be on {device}")
+
+
+def gemv(x: torch.Tensor, w: NVFP4Tensor, *, out: torch.Tensor | None = None, out_f32: torch.Tensor | None = None,
+         bias=None, mod_scale=None, mod_shift=None, gate=None, residual=None, act: int = ACT_NONE,
+         stream=None) -> torch.Tensor:
+    """y[M, N] = x W^T with the NVFP4 weight w [N, K] (as gemm's b) and 1..16 rows x [M, K] of bf16 that are not
+    quantized, then gemm's epilogue (bias, act, modulate, gate, residual); bf16 `out` [M, N] (rows may be strided)
+    and, when out_f32 is given, the same in float32 before the store."""
+    _require_cuda(x)
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1 or x.shape[1] != w.cols:
+        raise ValueError("gemv takes bf16 x [M, K] with unit column stride and K of the weight")
+    M, N = x.shape[0], w.rows
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    elif out.dtype != torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1:
+        raise ValueError("out is bf16 [M, N] with unit column stride")
+    _same_device(x.device, w.codes, out, out_f32, bias, mod_scale, mod_shift, gate, residual)
+    ep = None
+    if act or not (bias is mod_scale is mod_shift is gate is residual is out_f32 is None):
+        for v in (bias, mod_scale, mod_shift, gate):
+            if v is not None and (v.dtype != torch.bfloat16 or v.numel() != N or not v.is_contiguous()):
+                raise ValueError("bias, mod_scale, mod_shift and gate are contiguous bf16 [N]")
+        if residual is not None and (residual.dtype != torch.bfloat16 or residual.shape != (M, N) or
+                                     residual.stride(1) != 1):
+            raise ValueError("residual is bf16 [M, N] with unit column stride")
+        if out_f32 is not None and (out_f32.dtype != torch.float32 or out_f32.shape != (M, N) or
+                                    not out_f32.is_contiguous()):
+            raise ValueError("out_f32 is contiguous float32 [M, N]")
+        ep = ctypes.byref(make_epilogue(bias=bias, mod_scale=mod_scale, mod_shift=mod_shift, gate=gate,
+                                        residual=residual, act=act, debug_y=out_f32))
+    # a row stride means nothing for a single row
+    ldx, ldy = (x.stride(0), out.stride(0)) if M > 1 else (w.cols, N)
+    _check("nvfp4_gemv", _launch_on(x.device, stream, lib().nvfp4_gemv, x.data_ptr(), M, ldx, ctypes.byref(w.c()),
+                                    out.data_ptr(), ldy, ep))
+    return out
+
+
 class KVCache:
     """Paged NVFP4 KV cache: n_slots frame-chunks of tokens x heads x head_dim,
     K and V each stored as codes + row-major E4M3 scales + one binary32 tensor
@@ -422,6 +496,131 @@ class KVCache:
         _check("nvfp4_kv_attention", lib().nvfp4_kv_attention(
             ctypes.byref(cc), slots.data_ptr(), slots.numel(), q.data_ptr(), q.shape[0], float(scale),
             out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+        return out
+
+
+class PagedRows:
+    """The sequences of a step (nvfp4_paged_rows): sequence b owns rows row_start[b] .. row_start[b + 1] - 1 of the
+    step's row tensors, which are its last positions, lens[b] - n_b .. lens[b] - 1; pages[b] lists its cache pages.
+    Contiguous device int32 tensors [B + 1], [B] and [B, max_pages], read by the kernels at every call; n_rows (rows
+    of the row tensors), max_rows (most rows of a sequence) and max_len (longest sequence) are the host's bounds."""
+
+    def __init__(self, row_start: torch.Tensor, lens: torch.Tensor, pages: torch.Tensor, *, n_rows: int, max_rows: int,
+                 max_len: int):
+        _require_cuda(row_start, lens, pages)
+        for t in (row_start, lens, pages):
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError("row_start, lens and pages are contiguous int32 tensors")
+        B = lens.numel()
+        if row_start.shape != (B + 1,) or lens.dim() != 1 or pages.dim() != 2 or pages.shape[0] != B:
+            raise ValueError("row_start is [B + 1], lens [B], pages [B, max_pages]")
+        _same_device(lens.device, row_start, pages)
+        self.row_start, self.lens, self.pages = row_start, lens, pages
+        self.n_seqs, self.n_rows, self.max_rows, self.max_len = B, n_rows, max_rows, max_len
+        self._c = CPagedRows(row_start.data_ptr(), lens.data_ptr(), pages.data_ptr(), B, pages.shape[1], n_rows,
+                             max_rows, max_len)
+
+    def c(self) -> CPagedRows:
+        return self._c
+
+
+class PagedKVCache:
+    """NVFP4 cache of n_pages pages of page_size tokens x kv_heads x head_dim (64 or 128) for sequences that grow by
+    tokens: codes [n_pages, kv_heads, page_size, d / 2] and E4M3 scales [.., d / 16] of K and V, under one tensor
+    scale each for the whole cache (k_scale, v_scale: numbers or device float32 tensors; amax / 2688 of a
+    calibration).  The caller hands out the pages."""
+
+    def __init__(self, n_pages: int, page_size: int, kv_heads: int, head_dim: int, *, k_scale, v_scale, device="cuda"):
+        self.n_pages, self.page_size, self.kv_heads, self.head_dim = n_pages, page_size, kv_heads, head_dim
+        u8 = torch.uint8
+        shape = (n_pages, kv_heads, page_size)
+        self.k_codes = torch.zeros((*shape, head_dim // 2), dtype=u8, device=device)
+        self.v_codes = torch.zeros((*shape, head_dim // 2), dtype=u8, device=device)
+        self.k_scales = torch.zeros((*shape, head_dim // 16), dtype=u8, device=device)
+        self.v_scales = torch.zeros((*shape, head_dim // 16), dtype=u8, device=device)
+        self.device = self.k_codes.device
+        # (the cache keeps its own copies: a later change of the caller's tensors does not reach the pages written)
+        self.k_global = torch.as_tensor(k_scale, dtype=torch.float32, device=self.device).reshape(1).clone()
+        self.v_global = torch.as_tensor(v_scale, dtype=torch.float32, device=self.device).reshape(1).clone()
+        self.ws_rows = workspace(OP_PAGED_ROWS, device=self.device)
+        self._c = CPagedCache(self.k_codes.data_ptr(), self.k_scales.data_ptr(), self.v_codes.data_ptr(),
+                              self.v_scales.data_ptr(), self.k_global.data_ptr(), self.v_global.data_ptr(), n_pages,
+                              page_size, kv_heads, head_dim)
+
+    def c(self) -> CPagedCache:
+        return self._c
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in
+                   (self.k_codes, self.v_codes, self.k_scales, self.v_scales, self.k_global, self.v_global))
+
+    def _check_rows(self, rows: PagedRows, heads: int, what: str, *ts) -> None:
+        _same_device(self.device, rows.lens, *ts)
+        for t in ts:
+            if t.dtype != torch.bfloat16 or t.shape != (rows.n_rows, heads, self.head_dim) or (
+                    t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.head_dim))):
+                raise ValueError(f"{what} takes bf16 [n_rows, {heads}, {self.head_dim}] rows whose heads are contiguous")
+
+    def _ld(self, t: torch.Tensor) -> int:
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * self.head_dim
+
+    def append(self, rows: PagedRows, k: torch.Tensor, v: torch.Tensor, *, rope=None, ws: torch.Tensor | None = None,
+               stream=None) -> None:
+        """Quantize the rows' K and V (bf16 [n_rows, kv_heads, d], rows may be strided) into their pages.  rope =
+        (cos, sin), float32 [n_rows, d / 2] each: the keys are turned first (interleaved pairs, as KVCache.append)."""
+        self._check_rows(rows, self.kv_heads, "append", k, v)
+        cos, sin = rope if rope is not None else (None, None)
+        for t in (cos, sin):
+            if rope is not None and (t.dtype != torch.float32 or not t.is_contiguous() or
+                                     t.shape != (rows.n_rows, self.head_dim // 2)):
+                raise ValueError("rope tables are contiguous float32 [n_rows, d / 2]")
+        _same_device(self.device, cos, sin)
+        ws = self.ws_rows if ws is None else ws
+        _check("nvfp4_paged_append", _launch_on(
+            self.device, stream, lib().nvfp4_paged_append, ctypes.byref(self._c), ctypes.byref(rows._c), k.data_ptr(),
+            self._ld(k), v.data_ptr(), self._ld(v), _ptr(cos), _ptr(sin), ws.data_ptr(), ws.numel()))
+
+    def gather(self, rows: PagedRows, *, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+               ws: torch.Tensor | None = None, stream=None):
+        """Read the rows' K and V back to bf16 [n_rows, kv_heads, d]."""
+        shape = (rows.n_rows, self.kv_heads, self.head_dim)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        self._check_rows(rows, self.kv_heads, "gather", k_out, v_out)
+        ws = self.ws_rows if ws is None else ws
+        _check("nvfp4_paged_gather", _launch_on(
+            self.device, stream, lib().nvfp4_paged_gather, ctypes.byref(self._c), ctypes.byref(rows._c),
+            k_out.data_ptr(), self._ld(k_out), v_out.data_ptr(), self._ld(v_out), ws.data_ptr(), ws.numel()))
+        return k_out, v_out
+
+    def attention_workspace(self, rows: PagedRows, heads: int, *, window: int = 0, sinks: int = 0) -> torch.Tensor:
+        """A workspace for attention() with these arguments (and for any with fewer rows of the same bounds)."""
+        n = int(lib().nvfp4_paged_attention_workspace_bytes(ctypes.byref(self._c), ctypes.byref(rows._c), heads, window,
+                                                            sinks))
+        if n == 0:
+            raise ValueError("nvfp4_paged_attention_workspace_bytes: refused arguments")
+        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        ws[:256].zero_()
+        return ws
+
+    def attention(self, rows: PagedRows, q: torch.Tensor, *, window: int = 0, sinks: int = 0, scale: float = 0.0,
+                  out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Causal attention of the rows' queries (bf16 [n_rows, heads, d], rows may be strided) over their sequences'
+        cached keys and values: position p sees j <= p with j > p - window (window 0: all) or j < sinks."""
+        if q.dim() != 3:
+            raise ValueError("attention takes q [n_rows, heads, head_dim]")
+        heads = q.shape[1]
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        self._check_rows(rows, heads, "attention", q, out)
+        if ws is None:
+            ws = self.attention_workspace(rows, heads, window=window, sinks=sinks)
+        _check("nvfp4_paged_attention", _launch_on(
+            self.device, stream, lib().nvfp4_paged_attention, ctypes.byref(self._c), ctypes.byref(rows._c),
+            q.data_ptr(), self._ld(q), heads, window, sinks, scale, out.data_ptr(), self._ld(out), ws.data_ptr(),
+            ws.numel()))
         return out
 
 

@@ -93,7 +93,8 @@ enum {
     NVFP4_OP_LN_QUANTIZE = 4, /* nvfp4_ln_modulate_quantize (m = rows) */
     NVFP4_OP_QUANTIZE_2D = 5, /* nvfp4_quantize_2d */
     NVFP4_OP_QUANTIZE_T = 6,  /* nvfp4_quantize_t */
-    NVFP4_OP_KV_ATTENTION = 7 /* nvfp4_kv_attention */
+    NVFP4_OP_KV_ATTENTION = 7, /* nvfp4_kv_attention */
+    NVFP4_OP_PAGED_ROWS = 8 /* nvfp4_paged_append, nvfp4_paged_gather */
 };
 
 /* Workspace bytes the caller must pass to the call `op` (device memory,
@@ -264,6 +265,24 @@ typedef struct {
 nvfp4_status nvfp4_gemm(const nvfp4_tensor* A, const nvfp4_tensor* B, void* c_bf16, int64_t ldc,
                         const nvfp4_epilogue* ep, void* workspace, size_t ws_bytes, nvfp4_stream_t stream);
 
+/* Matrix-vector products with an NVFP4 weight: y[M x N] = a32_W * x (W_q . S_W)^T,
+ * then the epilogue, for the 1..16 rows of a token-by-token step; x stays bf16
+ * and is not quantized.  x_bf16: bf16 [m x K], row stride ldx (ldx >= K,
+ * ldx % 8 == 0, 16-byte aligned), 0 <= m <= 16 (else NVFP4_ERR_UNSUPPORTED:
+ * nvfp4_quantize and nvfp4_gemm take more rows).  W: the operand nvfp4_gemm
+ * takes as B ([N x K], K % 64 == 0, any N >= 1; both <= 2^30).
+ * y_bf16: bf16 [m x N], row stride ldy >= N, any 2-byte alignment, or NULL when
+ * ep->debug_y is set.  ep: as nvfp4_gemm's, in the same order (bias, act, modulate,
+ * gate, residual; here any 2-byte alignment, and GELU with the exact tanh);
+ * ep->debug_y receives y as binary32 [m x N].  The requant and out_amax fields
+ * must be unset (NVFP4_ERR_UNSUPPORTED) and debug_flags 0.  ep may be NULL.
+ * Products of binary16 operands: e2m1 * s is exact there; a row of x is scaled
+ * by a power of two per 128 columns, which rounds only values below 2^-28 of
+ * the largest of them.  Binary32 sums in a fixed order.  One launch, no
+ * workspace. */
+nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t m, int64_t ldx, const nvfp4_tensor* W, void* y_bf16, int64_t ldy,
+                        const nvfp4_epilogue* ep, nvfp4_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* NVFP4 KV cache  [RN-I] per-chunk K/V quantization; [NEWS] in-place update  */
 /* ------------------------------------------------------------------------ */
@@ -371,6 +390,93 @@ int32_t nvfp4_attention_chunks(int32_t t, int32_t sink_global, int32_t shot_star
 nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const int32_t* slots_dev, int32_t n, const void* q_bf16,
                                 int32_t tq, float scale, void* o_bf16, void* workspace, size_t ws_bytes,
                                 nvfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Paged NVFP4 cache: sequences that grow by tokens                           */
+/* ------------------------------------------------------------------------ */
+/* The slots above hold whole frame-chunks under the chunk's own tensor scale.
+ * Here a sequence grows by any number of tokens a step, so each of K and V has
+ * one tensor scale for the whole cache, given by the caller (as
+ * NVFP4_Q_GIVEN_GLOBAL: amax / 2688 of a calibration; larger values saturate),
+ * and the block scales follow each token.
+ * Row (p * kv_heads + h) * page_size + o is token o of page p, head h: its
+ * head_dim / 2 code bytes at that multiple in *_codes, its head_dim / 16 scale
+ * bytes in *_scales.  head_dim 64 or 128, page_size a multiple of 16 up to
+ * 2^20, kv_heads up to 2^16 (else NVFP4_ERR_UNSUPPORTED). */
+typedef struct {
+    void* k_codes;
+    void* k_scales;
+    void* v_codes;
+    void* v_scales;
+    const float* k_global; /* device binary32 */
+    const float* v_global; /* device binary32 */
+    int32_t n_pages, page_size, kv_heads, head_dim;
+} nvfp4_paged_cache;
+
+/* The sequences of a step.  Sequence b owns rows row_start[b] ..
+ * row_start[b + 1] - 1 of the step's row tensors ([n_rows][..]); with n_b of
+ * them, row i of the sequence is its position lens[b] - n_b + i: its last n_b
+ * positions, as the new tokens of a step are.  Position p lies in page
+ * pages[b * max_pages + p / page_size] at p % page_size.  The three arrays are
+ * device memory and are read by the kernels, so a captured call follows their
+ * contents.  Rows behind row_start[n_seqs] belong to no sequence and are left
+ * as they were.  n_b = 0 is a sequence that takes no part.
+ * max_rows and max_len bound n_b and lens[b] on the host's side: max_rows sizes
+ * the launch; max_len only guides how it is split (a longer sequence is still
+ * read whole).
+ * Reported as NVFP4_ERR_DEVICE (info = the sequence): a row range that is not
+ * ascending within [0, n_rows], a negative length, and for the attention more
+ * than max_rows rows (the sequence is skipped); a page entry that is needed and
+ * is not one of the cache's pages, or lies behind max_pages (its rows are
+ * skipped; its keys count as masked). */
+typedef struct {
+    const int32_t* row_start; /* [n_seqs + 1] */
+    const int32_t* lens;      /* [n_seqs] */
+    const int32_t* pages;     /* [n_seqs][max_pages] */
+    int32_t n_seqs, max_pages, n_rows, max_rows, max_len;
+} nvfp4_paged_rows;
+
+/* Quantizes the rows' keys and values (bf16 [n_rows][kv_heads][head_dim], ld_k
+ * / ld_v elements between rows, multiples of 8, so that slices of a fused
+ * projection will do) into their pages, by the quantize rule above under the
+ * cache's tensor scales.  rope_cos, rope_sin: device binary32 [n_rows][head_dim
+ * / 2] or both NULL: the keys are turned first, exactly as
+ * nvfp4_kv_append_rope does.  A row before its sequence's first position
+ * (lens[b] < n_b) is not written.  Two rows must not share a place: pages of
+ * two sequences may be the same only where neither writes.
+ * workspace: nvfp4_workspace_bytes(NVFP4_OP_PAGED_ROWS, 0, 0, 0) bytes.  One
+ * launch. */
+nvfp4_status nvfp4_paged_append(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows, const void* k_bf16,
+                                int64_t ld_k, const void* v_bf16, int64_t ld_v, const float* rope_cos,
+                                const float* rope_sin, void* workspace, size_t ws_bytes, nvfp4_stream_t stream);
+
+/* Reads the rows' keys and values back: bf16_rne(fl32(fl32(e2m1 * s) * a32)),
+ * zeros for a row before its sequence's first position.  With n_b = lens[b]
+ * whole sequences.  Otherwise as nvfp4_paged_append. */
+nvfp4_status nvfp4_paged_gather(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows, void* k_bf16,
+                                int64_t ld_k, void* v_bf16, int64_t ld_v, void* workspace, size_t ws_bytes,
+                                nvfp4_stream_t stream);
+
+/* Causal attention of the rows over their sequences in the cache (append them
+ * first: a row sees its own position).  The row at position p sees the keys
+ * j <= p with j > p - window or j < sinks; window 0: every j <= p.  q_bf16 and
+ * o_bf16: bf16 [n_rows][heads][head_dim], ld_q / ld_o elements between rows,
+ * multiples of 8; heads a multiple of kv_heads, query head h reads K/V head
+ * h / (heads / kv_heads).  scale 0: 1 / sqrt(head_dim).  Keys and values are
+ * the exact e2m1 * s * a32; queries are scaled by a power of two to binary16;
+ * binary32 accumulation and softmax; the weights go to the second product in
+ * binary16.  A row that sees no key gives zeros.  Pages that hold no visible
+ * key are not looked up, so a window's caller may have given them back.
+ * workspace: nvfp4_paged_attention_workspace_bytes of the same arguments (0:
+ * refused), which grows with n_rows; results do not depend on what it holds
+ * behind the control block.  One launch, or two when long sequences are split
+ * over CTAs. */
+size_t nvfp4_paged_attention_workspace_bytes(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows,
+                                             int32_t heads, int32_t window, int32_t sinks);
+nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows, const void* q_bf16,
+                                   int64_t ld_q, int32_t heads, int32_t window, int32_t sinks, float scale,
+                                   void* o_bf16, int64_t ld_o, void* workspace, size_t ws_bytes,
+                                   nvfp4_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Training-side operands  [RN-T] "NVFP4 训练的工程细节"                        */
