@@ -161,55 +161,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 32;  // keys of a tile
 constexpr int kWarps = 4;
-constexpr float kLazy = 8.0f;      // a reference maximum moves when exceeded by more than 2^8
-constexpr float kFloor = -1e30f;   // the reference before any visible key
-
-struct AttnArgs {
-    View v;
-    const uint8_t* q;  // bf16 [n_rows][heads][d], ld_q elements between rows
-    uint8_t* o;
-    int64_t ld_q, ld_o;
-    int heads, group, window, sinks, max_rows;
-    int row_tiles, splits, split_tiles;
-    float scale_log2;
-    float* part_o;   // [splits][n_rows][heads][d]
-    float2* part_ml; // [splits][n_rows][heads] (reference maximum, sum)
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-
-// Rows f0 .. f0 + cols - 1 of a sequence's n * group (row, query head) pairs.
-struct Rows {
-    int n;     // pairs in the unit
-    Span span;
-};
-
-__device__ __forceinline__ Rows unit_rows(const AttnArgs& a, const Seq& s, int f0, int cols) {
-    Rows r;
-    r.n = min(cols, s.n * a.group - f0);
-    if (r.n <= 0) {
-        r.n = 0;
-        r.span = Span{0, 0, 0};
-        return r;
-    }
-    const int p = s.len - s.n;
-    r.span = visible_span(p + f0 / a.group, p + (f0 + r.n - 1) / a.group, a.window, a.sinks);
-    return r;
-}
-
-// Tiles of one split of a unit with `count` tiles.
-__device__ __forceinline__ int tiles_per_split(const AttnArgs& a, int count) {
-    return max(a.split_tiles, (count + a.splits - 1) / a.splits);
 }
 
 template <int D>
@@ -646,7 +602,8 @@ nvfp4_status rows_call(bool append, const nvfp4_paged_cache* c, const nvfp4_page
 
 // How an attention call is cut up; the same for its workspace query.
 struct Plan {
-    int cols;  // (row, query head) pairs of a unit
+    bool chunks;  // chunk_kernel (paged_attention.cu), else decode_kernel
+    int cols;     // (row, query head) pairs of a unit
     int row_tiles, splits, split_tiles;
     int64_t units;
     size_t ws;
@@ -655,7 +612,10 @@ struct Plan {
 bool make_plan(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, int heads, int window, int sinks, Plan* p) {
     const int64_t pairs = (int64_t)r->max_rows * (heads / c->kv_heads);
     if (pairs >= ((int64_t)1 << 31)) return false;
-    p->cols = pairs <= 8 ? 8 : 16;
+    // More pairs than the decode kernel's 16 columns would read (and decode) the keys several times
+    p->chunks = pairs > 16;
+    p->cols = p->chunks ? kChunkRows : pairs <= 8 ? 8 : 16;
+    const int keys = p->chunks ? kChunkKeys : kKeys;
     const int64_t row_tiles = std::max<int64_t>(1, (pairs + p->cols - 1) / p->cols);
     p->units = row_tiles * c->kv_heads * std::max(1, r->n_seqs);
     if (p->units >= ((int64_t)1 << 31)) return false;
@@ -663,10 +623,11 @@ bool make_plan(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, int heads,
     // the most tiles that one unit can see
     const int64_t unit_rows = std::min<int64_t>(r->max_rows, p->cols);
     int64_t seen = r->max_len;
-    if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + unit_rows + sinks + 2 * kKeys);
-    const int64_t most = (seen + kKeys - 1) / kKeys;
-    // runs of tiles such that about eight CTAs an SM have work, none shorter than a tile a warp
-    const int64_t want = std::max<int64_t>(1, (int64_t)kSms * 8 / p->units);
+    if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + unit_rows + sinks + 2 * keys);
+    const int64_t most = (seen + keys - 1) / keys;
+    // runs of tiles such that about eight CTAs an SM have work, none shorter than a tile a warp; chunks: one CTA an
+    // SM, no run shorter than four tiles
+    const int64_t want = std::max<int64_t>(1, (int64_t)kSms * (p->chunks ? 1 : 8) / p->units);
     int64_t per = std::max<int64_t>(kWarps, (most + want - 1) / want);
     int64_t splits = std::max<int64_t>(1, (most + per - 1) / per);
     if (p->units * splits >= ((int64_t)1 << 31)) return false;
@@ -746,17 +707,23 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, co
     const int64_t slots = (int64_t)p.splits * rows->n_rows * heads;
     a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kControl);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * cache->head_dim);
-    void (*kern)(AttnArgs) = cache->head_dim == 128 ? (p.cols == 8 ? decode_kernel<128, 1> : decode_kernel<128, 2>)
-                                                    : (p.cols == 8 ? decode_kernel<64, 1> : decode_kernel<64, 2>);
-    kern<<<(unsigned)(p.units * p.splits), kWarps * 32, 0, (cudaStream_t)stream>>>(a);
+    if (p.chunks) {
+        st = launch_chunks(a, p.units * p.splits, (cudaStream_t)stream);
+        if (st != NVFP4_OK) return st;
+    } else {
+        void (*kern)(AttnArgs) = cache->head_dim == 128 ? (p.cols == 8 ? decode_kernel<128, 1> : decode_kernel<128, 2>)
+                                                        : (p.cols == 8 ? decode_kernel<64, 1> : decode_kernel<64, 2>);
+        kern<<<(unsigned)(p.units * p.splits), kWarps * 32, 0, (cudaStream_t)stream>>>(a);
+    }
     if (p.splits > 1) {
         const int64_t warps = (int64_t)rows->n_seqs * rows->max_rows * heads;
         const int64_t grid = (warps + 3) / 4;
         if (grid >= ((int64_t)1 << 31)) return NVFP4_ERR_UNSUPPORTED;
-        if (cache->head_dim == 128)
-            combine_kernel<128, kKeys><<<(unsigned)grid, 128, 0, (cudaStream_t)stream>>>(a, p.cols);
-        else
-            combine_kernel<64, kKeys><<<(unsigned)grid, 128, 0, (cudaStream_t)stream>>>(a, p.cols);
+        void (*join)(AttnArgs, int) = p.chunks ? (cache->head_dim == 128 ? combine_kernel<128, kChunkKeys>
+                                                                         : combine_kernel<64, kChunkKeys>)
+                                               : (cache->head_dim == 128 ? combine_kernel<128, kKeys>
+                                                                         : combine_kernel<64, kKeys>);
+        join<<<(unsigned)grid, 128, 0, (cudaStream_t)stream>>>(a, p.cols);
     }
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }

@@ -96,5 +96,52 @@ __device__ __forceinline__ bool group_seen(const Span& s, int k0) {
     return k0 < s.hi && (k0 + kGroup > s.lo || k0 < s.sink_end);
 }
 
+// ---------------------------------------------------------------------------
+// attention: what the kernel for few rows and the one for chunks share
+// ---------------------------------------------------------------------------
+constexpr float kLazy = 8.0f;     // a reference maximum moves when exceeded by more than 2^8
+constexpr float kFloor = -1e30f;  // the reference before any visible key
+
+struct AttnArgs {
+    View v;
+    const uint8_t* q;  // bf16 [n_rows][heads][d], ld_q elements between rows
+    uint8_t* o;
+    int64_t ld_q, ld_o;
+    int heads, group, window, sinks, max_rows;
+    int row_tiles, splits, split_tiles;
+    float scale_log2;
+    float* part_o;   // [splits][n_rows][heads][d]
+    float2* part_ml; // [splits][n_rows][heads] (reference maximum, sum)
+};
+
+// Rows f0 .. f0 + cols - 1 of a sequence's n * group (row, query head) pairs.
+struct Rows {
+    int n;     // pairs in the unit
+    Span span;
+};
+
+__device__ __forceinline__ Rows unit_rows(const AttnArgs& a, const Seq& s, int f0, int cols) {
+    Rows r;
+    r.n = min(cols, s.n * a.group - f0);
+    if (r.n <= 0) {
+        r.n = 0;
+        r.span = Span{0, 0, 0};
+        return r;
+    }
+    const int p = s.len - s.n;
+    r.span = visible_span(p + f0 / a.group, p + (f0 + r.n - 1) / a.group, a.window, a.sinks);
+    return r;
+}
+
+// Tiles of one split of a unit with `count` tiles.
+__device__ __forceinline__ int tiles_per_split(const AttnArgs& a, int count) {
+    return max(a.split_tiles, (count + a.splits - 1) / a.splits);
+}
+
+// The kernel for chunks (paged_attention.cu).
+constexpr int kChunkRows = 256;  // (row, query head) pairs of a unit
+constexpr int kChunkKeys = 128;
+nvfp4_status launch_chunks(const AttnArgs& a, int64_t units, cudaStream_t stream);
+
 }  // namespace paged
 }  // namespace nvfp4

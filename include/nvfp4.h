@@ -428,7 +428,7 @@ typedef struct {
  * ascending within [0, n_rows], a negative length, and for the attention more
  * than max_rows rows (the sequence is skipped); a page entry that is needed and
  * is not one of the cache's pages, or lies behind max_pages (its rows are
- * skipped; its keys count as masked). */
+ * skipped; the attention of that sequence is then not meaningful). */
 typedef struct {
     const int32_t* row_start; /* [n_seqs + 1] */
     const int32_t* lens;      /* [n_seqs] */
@@ -469,8 +469,11 @@ nvfp4_status nvfp4_paged_gather(const nvfp4_paged_cache* cache, const nvfp4_page
  * key are not looked up, so a window's caller may have given them back.
  * workspace: nvfp4_paged_attention_workspace_bytes of the same arguments (0:
  * refused), which grows with n_rows; results do not depend on what it holds
- * behind the control block.  One launch, or two when long sequences are split
- * over CTAs. */
+ * behind the control block.  Up to 16 (row, query head) pairs a K/V head
+ * (max_rows * heads / kv_heads) run on a kernel for decode steps, more on one
+ * for chunks (tcgen05), whose waits are bounded: one that runs out records
+ * NVFP4_ERR_TIMEOUT (info = which wait) and leaves o incomplete.  One launch, or
+ * two when long sequences are split over CTAs. */
 size_t nvfp4_paged_attention_workspace_bytes(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows,
                                              int32_t heads, int32_t window, int32_t sinks);
 nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows, const void* q_bf16,
