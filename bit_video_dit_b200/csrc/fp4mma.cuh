@@ -1,6 +1,6 @@
-// fp4mma.cuh -- E2M1 data as operands of the binary16 warp-level matrix
-// instruction (16 x 8 x 16), for kernels with few rows: decoding, and the
-// scaling of bf16 rows to binary16.
+// fp4mma.cuh -- E2M1 data as operands of the 16-bit matrix instructions:
+// decoding, the 16 x 8 x 16 warp-level product, and the scaling of bf16 rows to
+// binary16.
 #pragma once
 
 #include "common.cuh"
@@ -20,66 +20,78 @@ __device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Decoded operands carry 2^-kDecodeShift: v = 2^-8 e2m1 s, exact in binary16
-// (a multiple of 2^-18 below 2^4).  There are two ways to the same value, and
-// the kernels use both, since the conversion unit alone or the integer pipe
-// alone would bound them (44 and 41 elements a clock and SM measured):
-//  - the conversion instruction and a multiplication by 2^-8 s;
-//  - shifts and masks that put a code's sign, exponent and fraction at their
-//    places in binary16, which is 2^-14 e2m1, and a multiplication by 2^6 s.
-constexpr uint32_t kMulCvt = 0x1C001C00u;  // 2^-8 twice
-constexpr uint32_t kMulBits = 0x54005400u;  // 2^6 twice
-constexpr float kDecodeBack = 256.0f;       // 2^8
-
-// 8 codes (two a byte) -> the pairs (0, 1), (2, 3), (4, 5), (6, 7); s = 2^-8 scale
-__device__ __forceinline__ void decode8_cvt(uint32_t w, __half2 s, uint32_t* o) {
+// 8 codes, two a byte, times the pair s: e2m1 s is exact in binary16 (at most 6
+// significant bits).  Naming the word's bytes lets each conversion read its
+// byte in place: 2 instructions a pair, 136 elements a nanosecond and SM
+// measured, against 78 with a shift and mask a byte, and 70 with shifts and
+// masks in place of the conversion.
+__device__ __forceinline__ void decode8(uint32_t w, __half2 s, uint32_t* o) {
+    asm("{\n\t"
+        ".reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t"
+        "}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
 #pragma unroll
-    for (int i = 0; i < 4; i++) o[i] = h2_bits(__hmul2(e2m1x2_to_half2((w >> (8 * i)) & 0xFFu), s));
+    for (int i = 0; i < 4; i++) o[i] = h2_bits(__hmul2(bits_h2(o[i]), s));
 }
 
-// 8 codes -> the pairs (i, i + 4), i = 0..3; s = 2^6 scale
-__device__ __forceinline__ void decode8_bits(uint32_t w, __half2 s, uint32_t* o) {
+// The 8 codes of one row and of another -> the 8 pairs (a_i s.x, b_i s.y)
+__device__ __forceinline__ void decode8_rows(uint32_t a, uint32_t b, __half2 s, uint32_t* o) {
+    uint32_t even[4], odd[4];
+    decode8((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), s, even);
+    decode8(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), s, odd);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const uint32_t y = w << (12 - 4 * i);
-        o[i] = h2_bits(__hmul2(bits_h2((y & 0x80008000u) | ((y >> 3) & 0x0E000E00u)), s));
+        o[2 * i] = even[i];
+        o[2 * i + 1] = odd[i];
     }
 }
 
-// One lane's 8 NW bf16 of a row, whose other lanes are t ^ 1, t ^ 2, times 2^k
-// with the row's largest magnitude in [2^14, 2^15), as binary16 pairs in the
-// order of the decoded operand: decode8_cvt's for the first NW / 2 words of 8,
-// decode8_bits's for the rest.  Exact for values down to 2^-28 of the largest
-// (bf16 has 8 significant bits).  Returns 2^-k.
-template <int NW>
-__device__ __forceinline__ float scale_row(const uint4* v, uint32_t* o) {
+// The largest magnitude (bf16 bits) of 8 N bf16.
+template <int N>
+__device__ __forceinline__ uint32_t max_bits(const uint4* v) {
     uint32_t mx = 0u;
 #pragma unroll
-    for (int i = 0; i < NW; i++)
+    for (int i = 0; i < N; i++)
         mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
                                    __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
-    mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-    mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-    mx = max(mx & 0xFFFFu, mx >> 16);
+    return max(mx & 0xFFFFu, mx >> 16);
+}
+
+// 2^k that brings a row's largest magnitude into [2^14, 2^15), and 2^-k.
+// Rounding to binary16 is then exact for values down to 2^-28 of the largest
+// (bf16 has 8 significant bits).
+struct RowScale {
+    float up, down;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t mx) {
     const int k = mx == 0u ? 0 : min(126, 141 - (int)(mx >> 7));
-    const float pk = __uint_as_float((uint32_t)(127 + k) << 23);
+    return RowScale{__uint_as_float((uint32_t)(127 + k) << 23), __uint_as_float((uint32_t)(127 - k) << 23)};
+}
+
+// 8 bf16 times 2^k -> 4 binary16 pairs
+__device__ __forceinline__ void scale8(const uint4& v, float up, uint32_t* o) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < NW; j++) {
-        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+    for (int i = 0; i < 4; i++)
+        o[i] = h2_bits(__floats2half2_rn(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up));
+}
+
+// One lane's 8 N bf16 of a row whose other lanes are t ^ 1 and t ^ 2; returns 2^-k.
+template <int N>
+__device__ __forceinline__ float scale_row(const uint4* v, uint32_t* o) {
+    uint32_t mx = max_bits<N>(v);
+    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+    const RowScale s = row_scale(mx);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            float lo, hi;
-            if (j < NW / 2) {  // 8 j + 2 i, + 1
-                lo = __uint_as_float(w[i] << 16);
-                hi = __uint_as_float(w[i] & 0xFFFF0000u);
-            } else {  // 8 j + i, 8 j + i + 4
-                lo = (i & 1) ? __uint_as_float(w[i >> 1] & 0xFFFF0000u) : __uint_as_float(w[i >> 1] << 16);
-                hi = (i & 1) ? __uint_as_float(w[2 + (i >> 1)] & 0xFFFF0000u) : __uint_as_float(w[2 + (i >> 1)] << 16);
-            }
-            o[4 * j + i] = h2_bits(__floats2half2_rn(lo * pk, hi * pk));
-        }
-    }
-    return __uint_as_float((uint32_t)(127 - k) << 23);
+    for (int j = 0; j < N; j++) scale8(v[j], s.up, o + 4 * j);
+    return s.down;
 }
 
 }  // namespace fp4mma

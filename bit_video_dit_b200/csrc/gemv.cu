@@ -83,12 +83,12 @@ __device__ __forceinline__ void load_chunk(const Args& a, int row0, int c, int g
 
 // 32 codes of one row with their two block scales -> 16 operand pairs
 __device__ __forceinline__ void decode32(const uint4& c, uint32_t two_scales, uint32_t* o) {
-    const __half2 s = __hmul2(e4m3x2_to_half2((uint16_t)two_scales), bits_h2((kMulBits << 16) | (kMulCvt & 0xFFFFu)));
+    const __half2 s = e4m3x2_to_half2((uint16_t)two_scales);
     const __half2 s0 = __low2half2(s), s1 = __high2half2(s);
-    decode8_cvt(c.x, s0, o);
-    decode8_cvt(c.y, s0, o + 4);
-    decode8_bits(c.z, s1, o + 8);
-    decode8_bits(c.w, s1, o + 12);
+    decode8(c.x, s0, o);
+    decode8(c.y, s0, o + 4);
+    decode8(c.z, s1, o + 8);
+    decode8(c.w, s1, o + 12);
 }
 
 __device__ __forceinline__ float act_gelu(float y) {
@@ -103,7 +103,7 @@ __device__ __forceinline__ float peer_f32(const float* p, uint32_t rank) {
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) gemv_kernel(const __grid_constant__ Args a) {
     __shared__ float part[kWarps][8 * NT][kPitch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int rank = a.cluster == 1 ? 0 : (int)(blockIdx.x % (unsigned)a.cluster);
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const __grid_constant
         }
         cluster_sync_all();
     }
-    const float alpha = __ldg(a.a32) * kDecodeBack;
+    const float alpha = __ldg(a.a32);
     const int share = (outs + a.cluster - 1) / a.cluster;
     const int last = min(outs, (rank + 1) * share);
     for (int o = rank * share + threadIdx.x; o < last; o += kThreads) {

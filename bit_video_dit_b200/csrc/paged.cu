@@ -89,10 +89,12 @@ __device__ __forceinline__ void gather_block(const RowArgs& a, int t, int row, i
         const uint32_t sc = __ldg(v.scales[t] + at * (v.d / 16) + blk);
         const __half2 s2 = e4m3x2_to_half2((uint16_t)(sc | (sc << 8)));
         const float a32 = __ldg(v.a32[t]);
+        uint32_t h[8];
+        decode8(c.x, s2, h);
+        decode8(c.y, s2, h + 4);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const float2 f =
-                __half22float2(__hmul2(e2m1x2_to_half2(((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu), s2));
+            const float2 f = __half22float2(bits_h2(h[i]));
             const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(f.x, a32), __fmul_rn(f.y, a32));
             o[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
@@ -168,103 +170,113 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
+// Page of the 16 keys from kq on: -1 when no row of the unit sees one of them
+// (not looked up), else what the table lists (-2 behind its end).
+__device__ __forceinline__ int group_page(const View& v, const int32_t* table, const Span& sp, int kq) {
+    if (!group_seen(sp, kq)) return -1;
+    const int i = v.page_shift >= 0 ? kq >> v.page_shift : kq / v.page_size;
+    return i < v.max_pages ? __ldg(table + i) : -2;
+}
+
+// One lane's share of a 32-key tile.
 template <int D>
 struct KVTile {
-    uint4 k[2][2];     // keys 16 q + g, + 8: 8 * D / 32 codes from D / 4 * t (D = 64: .x, .y)
-    uint32_t ks[2];    // their scales: key g in bits 15:0, key g + 8 in 31:16
-    uint2 v[2][4];     // keys 16 q + 2 t + {0, 1, 8, 9}: D / 8 codes from D / 8 * g (D = 64: .x)
-    uint32_t vs[2];    // their scales, one a byte
-    bool ok[2];        // the 16 keys lie in a page of the cache
+    uint32_t k[2][2][D / 32];  // keys 16 q + g, + 8: the codes of channels D / 4 t ..
+    uint32_t ks[2][2];         // their scales: two blocks (D = 64: one, twice) in bits 15:0
+    uint32_t v[2][4][D / 64];  // keys 16 q + 2 t + {0, 1, 8, 9}: the codes of channels D / 8 g ..
+    uint32_t vs[2][4];         // their scale
+    bool ok[2];                // the 16 keys lie in a page of the cache
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+    if (N == 4) {
+        const uint4 x = ld_stream16(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if (N == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+        w[0] = x.x, w[1] = x.y;
+    } else {
+        w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    }
+}
+
+// The lane's places in the cache for one head: add row * (D / 2) to a codes
+// pointer, row * (D / 16) to a scales pointer.
+struct Lane {
+    const uint8_t *kc, *ks, *vc, *vs;
+    uint32_t page_rows, head_row;  // rows of a page over all heads, of the heads before this one
 };
 
 template <int D>
-__device__ __forceinline__ void load_tile(const View& v, int b, int head, const Span& sp, int k0, int g, int t,
-                                          KVTile<D>& x) {
+__device__ __forceinline__ void load_tile(const View& v, const Lane& ln, int b, const Span& sp, int k0, int t,
+                                          const int* pages, KVTile<D>& x) {
 #pragma unroll
     for (int q = 0; q < 2; q++) {
         const int kq = k0 + 16 * q;
-        const int page = group_seen(sp, kq) ? page_of(v, b, kq) : -1;
-        x.ok[q] = page >= 0;
-        if (page >= 0) {
-            const int64_t r = cache_row(v, page, head, kq);
-            const uint8_t* kc = v.codes[0] + r * (D / 2) + D / 8 * t;
-            const uint8_t* vc = v.codes[1] + (r + 2 * t) * (D / 2) + D / 16 * g;
-            const uint8_t* ks = v.scales[0] + r * (D / 16);
-            const uint8_t* vs = v.scales[1] + (r + 2 * t) * (D / 16) + (D == 128 ? g : g / 2);
-            if (D == 128) {
-                x.k[q][0] = ld_stream16(kc + g * 64);
-                x.k[q][1] = ld_stream16(kc + (g + 8) * 64);
-                x.ks[q] = __ldg(reinterpret_cast<const uint16_t*>(ks + g * 8 + 2 * t)) |
-                          ((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(ks + (g + 8) * 8 + 2 * t)) << 16);
-            } else {
-                const uint2 k0v = __ldg(reinterpret_cast<const uint2*>(kc + g * 32));
-                const uint2 k1v = __ldg(reinterpret_cast<const uint2*>(kc + (g + 8) * 32));
-                x.k[q][0] = make_uint4(k0v.x, k0v.y, 0u, 0u);
-                x.k[q][1] = make_uint4(k1v.x, k1v.y, 0u, 0u);
-                const uint32_t s0 = __ldg(ks + g * 4 + t), s1 = __ldg(ks + (g + 8) * 4 + t);
-                x.ks[q] = (s0 | (s0 << 8)) | ((s1 | (s1 << 8)) << 16);
+        x.ok[q] = (unsigned)pages[q] < (unsigned)v.n_pages;
+        if (x.ok[q]) {
+            const int at = v.page_shift >= 0 ? kq & (v.page_size - 1) : kq % v.page_size;
+            const uint32_t row = (uint32_t)pages[q] * ln.page_rows + ln.head_row + (uint32_t)at;  // below 2^32 (host)
+            const uint8_t* kc = ln.kc + (uint64_t)row * (D / 2);
+            const uint8_t* vc = ln.vc + (uint64_t)row * (D / 2);
+            const uint8_t* ks = ln.ks + (uint64_t)row * (D / 16);
+            const uint8_t* vs = ln.vs + (uint64_t)row * (D / 16);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                load_words<D / 32>(kc + 8 * h * (D / 2), x.k[q][h]);
+                if (D == 128) x.ks[q][h] = __ldg(reinterpret_cast<const uint16_t*>(ks + 8 * h * 8));
+                else x.ks[q][h] = __ldg(ks + 8 * h * 4) * 0x101u;
             }
-            uint32_t s4 = 0u;
+            if (kq + kGroup <= sp.hi) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int key = (i & 1) + 8 * (i >> 1);  // + 2 t
+                    load_words<D / 64>(vc + key * (D / 2), x.v[q][i]);
+                    x.vs[q][i] = __ldg(vs + key * (D / 16));
+                }
+            } else {  // what lies behind the last key is not a value
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int key = (i & 1) + 8 * (i >> 1);
+                    x.vs[q][i] = 0u;
+#pragma unroll
+                    for (int e = 0; e < D / 64; e++) x.v[q][i][e] = 0u;
+                    if (kq + 2 * t + key < sp.hi) {
+                        load_words<D / 64>(vc + key * (D / 2), x.v[q][i]);
+                        x.vs[q][i] = __ldg(vs + key * (D / 16));
+                    }
+                }
+            }
+        } else {
+            if (pages[q] != -1) record_error(v.err, NVFP4_ERR_DEVICE, (uint32_t)b);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                x.ks[q][h] = 0u;
+#pragma unroll
+                for (int e = 0; e < D / 32; e++) x.k[q][h][e] = 0u;
+            }
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const int key = (i & 1) + 8 * (i >> 1);  // + 2 t
-                const bool in = kq + 2 * t + key < sp.hi;  // what lies behind the last key is not a value
-                if (D == 128)
-                    x.v[q][i] = in ? __ldg(reinterpret_cast<const uint2*>(vc + key * 64)) : make_uint2(0u, 0u);
-                else
-                    x.v[q][i] = make_uint2(in ? __ldg(reinterpret_cast<const uint32_t*>(vc + key * 32)) : 0u, 0u);
-                s4 |= (in ? (uint32_t)__ldg(vs + key * (D / 16)) : 0u) << (8 * i);
+                x.vs[q][i] = 0u;
+#pragma unroll
+                for (int e = 0; e < D / 64; e++) x.v[q][i][e] = 0u;
             }
-            x.vs[q] = s4;
-        } else {
-            x.k[q][0] = x.k[q][1] = make_uint4(0u, 0u, 0u, 0u);
-            x.ks[q] = x.vs[q] = 0u;
-#pragma unroll
-            for (int i = 0; i < 4; i++) x.v[q][i] = make_uint2(0u, 0u);
         }
     }
 }
 
-// One key row's D / 4 codes and its scales (bits 15:0: two blocks, or one twice) -> D / 8 pairs
+// One key's D / 4 codes and their scales -> D / 8 pairs
 template <int D>
-__device__ __forceinline__ void decode_k(const uint4& c, uint32_t sc, uint32_t* o) {
-    const __half2 s = __hmul2(e4m3x2_to_half2((uint16_t)sc), bits_h2((kMulBits << 16) | (kMulCvt & 0xFFFFu)));
+__device__ __forceinline__ void decode_k(const uint32_t* c, uint32_t sc, uint32_t* o) {
+    const __half2 s = e4m3x2_to_half2((uint16_t)sc);
     const __half2 s0 = __low2half2(s), s1 = __high2half2(s);
-    if (D == 128) {
-        decode8_cvt(c.x, s0, o);
-        decode8_cvt(c.y, s0, o + 4);
-        decode8_bits(c.z, s1, o + 8);
-        decode8_bits(c.w, s1, o + 12);
-    } else {
-        decode8_cvt(c.x, s0, o);
-        decode8_bits(c.y, s1, o + 4);
-    }
-}
-
-// The same 8 codes of keys a and b -> pairs (a_i, b_i), i = 0..7.
-__device__ __forceinline__ void decode_v_bits(uint32_t wa, uint32_t wb, __half2 s, uint32_t* o) {
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-        const uint32_t x = __byte_perm(wa, wb, h ? 0x7632 : 0x5410);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint32_t y = x << (12 - 4 * i);
-            o[4 * h + i] = h2_bits(__hmul2(bits_h2((y & 0x80008000u) | ((y >> 3) & 0x0E000E00u)), s));
-        }
-    }
-}
-__device__ __forceinline__ void decode_v_cvt(uint32_t wa, uint32_t wb, __half2 s, uint32_t* o) {
-    const uint32_t e = (wa & 0x0F0F0F0Fu) | ((wb << 4) & 0xF0F0F0F0u);
-    const uint32_t d = ((wa >> 4) & 0x0F0F0F0Fu) | (wb & 0xF0F0F0F0u);
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        o[2 * i] = h2_bits(__hmul2(e2m1x2_to_half2((e >> (8 * i)) & 0xFFu), s));
-        o[2 * i + 1] = h2_bits(__hmul2(e2m1x2_to_half2((d >> (8 * i)) & 0xFFu), s));
-    }
+    for (int w = 0; w < D / 32; w++) decode8(c[w], w < D / 64 ? s0 : s1, o + 4 * w);
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32) decode_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int kCols = 8 * NT, kSteps = D / 16, kPer = D / 8;  // kPer: a lane's channels of O
     __shared__ float so[kWarps][kCols][D + 4];
     __shared__ float2 sml[kWarps][kCols];
@@ -287,12 +299,34 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const __grid_consta
     const Tiles<kKeys> tiles(rows.span);
     const int per = tiles_per_split(a, tiles.count);
     const int begin = split * per, end = min(tiles.count, begin + per);
-    if (a.splits > 1 && begin >= end && split > 0) return;
+    if (split > 0 && begin >= end) return;
 
-    // queries: column n of tile j is row f0 + 8 j + n
+    Lane ln;
+    ln.kc = v.codes[0] + g * (D / 2) + D / 8 * t;
+    ln.ks = v.scales[0] + g * (D / 16) + D / 64 * t;
+    ln.vc = v.codes[1] + 2 * t * (D / 2) + D / 16 * g;
+    ln.vs = v.scales[1] + 2 * t * (D / 16) + (D == 128 ? g : g / 2);
+    ln.page_rows = (uint32_t)v.kv_heads * (uint32_t)v.page_size;
+    ln.head_row = (uint32_t)head * (uint32_t)v.page_size;
+    const int32_t* table = v.pages + (int64_t)b * v.max_pages;
+
+    // pages are looked up two tiles ahead, their data loaded one tile ahead
+    KVTile<D> x;
+    int pages[2] = {-1, -1};
+    if (begin + warp < end) {
+        const int k0 = tiles.key0(begin + warp);
+        const int first[2] = {group_page(v, table, rows.span, k0), group_page(v, table, rows.span, k0 + 16)};
+        load_tile<D>(v, ln, b, rows.span, k0, t, first, x);
+        if (begin + warp + kWarps < end) {
+            const int k1 = tiles.key0(begin + warp + kWarps);
+            pages[0] = group_page(v, table, rows.span, k1);
+            pages[1] = group_page(v, table, rows.span, k1 + 16);
+        }
+    }
+
+    // queries: column n of tile j is row f0 + 8 j + n; columns past the last row are zeros and nobody reads them
     uint32_t qb[NT][D / 8];
     float c_col[NT][2];
-    int lo_col[NT][2], hi_col[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; j++) {
         uint4 raw[D / 32];
@@ -302,26 +336,22 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const __grid_consta
             a.q + ((int64_t)(s.first + f / a.group) * a.ld_q + (int64_t)(head * a.group + f % a.group) * D + D / 4 * t) * 2);
 #pragma unroll
         for (int i = 0; i < D / 32; i++) raw[i] = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-        const float back = scale_row<D / 32>(raw, qb[j]);
+        const float down = scale_row<D / 32>(raw, qb[j]) * (__ldg(v.a32[0]) * a.scale_log2);
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
-            c_col[j][e] = __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4 * e) * (__ldg(v.a32[0]) * a.scale_log2 * kDecodeBack);
-            const int n = 8 * j + 2 * t + e;
-            const int p = s.len - s.n + (f0 + n) / a.group;
-            hi_col[j][e] = n < rows.n ? p + 1 : 0;
-            lo_col[j][e] = a.window > 0 ? p - a.window + 1 : 0;
-        }
+        for (int e = 0; e < 2; e++) c_col[j][e] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4 * e);
     }
     const int p_first = s.len - s.n + f0 / a.group;  // the unit's first and last positions
     const int p_last = s.len - s.n + (f0 + rows.n - 1) / a.group;
 
-    float m[NT][2], l[NT][2], o[NT][kSteps][4];
+    // a column's reference maximum m as -m, and what an exponent relative to it must exceed for m to move; before
+    // its first visible key m is 0 and any exponent does
+    float nm[NT][2], limit[NT][2], l[NT][2], o[NT][kSteps][4];
 #pragma unroll
     for (int j = 0; j < NT; j++) {
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-            m[j][e] = kFloor;
-            l[j][e] = 0.0f;
+            nm[j][e] = l[j][e] = 0.0f;
+            limit[j][e] = -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < kSteps; i++)
@@ -329,18 +359,25 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const __grid_consta
             for (int e = 0; e < 4; e++) o[j][i][e] = 0.0f;
     }
 
-    KVTile<D> x;
-    if (begin + warp < end) load_tile<D>(v, b, head, rows.span, tiles.key0(begin + warp), g, t, x);
+#pragma unroll 2
     for (int i = begin + warp; i < end; i += kWarps) {
         const int k0 = tiles.key0(i);
         KVTile<D> next;
-        if (i + kWarps < end) load_tile<D>(v, b, head, rows.span, tiles.key0(i + kWarps), g, t, next);
+        if (i + kWarps < end) {
+            load_tile<D>(v, ln, b, rows.span, tiles.key0(i + kWarps), t, pages, next);
+            if (i + 2 * kWarps < end) {
+                const int k2 = tiles.key0(i + 2 * kWarps);
+                pages[0] = group_page(v, table, rows.span, k2);
+                pages[1] = group_page(v, table, rows.span, k2 + 16);
+            }
+        }
+        // z: the scores' exponents, relative to the reference: 2^z is the weight
         float z[2][NT][4];
 #pragma unroll
         for (int q = 0; q < 2; q++) {
             uint32_t ka[D / 8], kb[D / 8];
-            decode_k<D>(x.k[q][0], x.ks[q] & 0xFFFFu, ka);
-            decode_k<D>(x.k[q][1], x.ks[q] >> 16, kb);
+            decode_k<D>(x.k[q][0], x.ks[q][0], ka);
+            decode_k<D>(x.k[q][1], x.ks[q][1], kb);
 #pragma unroll
             for (int j = 0; j < NT; j++) {
 #pragma unroll
@@ -348,44 +385,60 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const __grid_consta
 #pragma unroll
                 for (int e = 0; e < kSteps; e++)
                     mma_16816(z[q][j], ka[2 * e], kb[2 * e], ka[2 * e + 1], kb[2 * e + 1], qb[j][2 * e], qb[j][2 * e + 1]);
-#pragma unroll
-                for (int e = 0; e < 4; e++) z[q][j][e] *= c_col[j][e & 1];
             }
         }
-        // every key of the tile seen by every row, or else key by key
-        const bool all = x.ok[0] && x.ok[1] && k0 + kKeys - 1 <= p_first &&
-                         (a.window == 0 || k0 > p_last - a.window || k0 + kKeys <= a.sinks);
-        if (!all || rows.n < kCols) {
-#pragma unroll
-            for (int q = 0; q < 2; q++)
-#pragma unroll
-                for (int j = 0; j < NT; j++)
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int key = k0 + 16 * q + g + 8 * (e >> 1);
-                        const bool seen = x.ok[q] && key < hi_col[j][e & 1] && (key >= lo_col[j][e & 1] || key < a.sinks);
-                        if (!seen) z[q][j][e] = -INFINITY;
-                    }
-        }
-        bool over = false;
 #pragma unroll
         for (int q = 0; q < 2; q++)
 #pragma unroll
             for (int j = 0; j < NT; j++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) over |= z[q][j][e] > m[j][e & 1] + kLazy;
+                for (int e = 0; e < 4; e++) z[q][j][e] = fmaf(z[q][j][e], c_col[j][e & 1], nm[j][e & 1]);
+        // every key of the tile seen by every row, or else key by key
+        const bool all = x.ok[0] && x.ok[1] && k0 + kKeys - 1 <= p_first &&
+                         (a.window == 0 || k0 > p_last - a.window || k0 + kKeys <= a.sinks);
+        if (!all) {
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const int p = s.len - s.n + (f0 + 8 * j + 2 * t + e) / a.group;
+                    const int lo = a.window > 0 ? p - a.window + 1 : 0;
+#pragma unroll
+                    for (int q = 0; q < 2; q++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const int key = k0 + 16 * q + g + 8 * h;
+                            if (!(x.ok[q] && key <= p && (key >= lo || key < a.sinks))) z[q][j][2 * h + e] = -INFINITY;
+                        }
+                }
+        }
+        float top[NT][2];
+        bool over = false;
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                top[j][e] = fmaxf(fmaxf(z[0][j][e], z[0][j][e + 2]), fmaxf(z[1][j][e], z[1][j][e + 2]));
+                over |= top[j][e] > limit[j][e];
+            }
         if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
             for (int j = 0; j < NT; j++)
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    float mx = fmaxf(fmaxf(z[0][j][e], z[0][j][e + 2]), fmaxf(z[1][j][e], z[1][j][e + 2]));
+                    float mx = top[j][e];
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-                    if (mx > m[j][e] + kLazy) {
-                        const float f = ex2(m[j][e] - mx);
-                        m[j][e] = mx;
+                    if (mx > limit[j][e]) {
+                        const float f = limit[j][e] == kLazy ? ex2(-mx) : 0.0f;
+                        limit[j][e] = kLazy;
+                        nm[j][e] -= mx;
                         l[j][e] *= f;
+#pragma unroll
+                        for (int q = 0; q < 2; q++) {
+                            z[q][j][e] -= mx;
+                            z[q][j][e + 2] -= mx;
+                        }
 #pragma unroll
                         for (int r = 0; r < kSteps; r++) {
                             o[j][r][e] *= f;
@@ -402,23 +455,21 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const __grid_consta
                 float p[4];
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    p[e] = ex2(z[q][j][e] - m[j][e & 1]);
+                    p[e] = ex2(z[q][j][e]);
                     l[j][e & 1] += p[e];
                 }
                 // the weights go to the tensor cores in binary16 (2^-11 of each)
                 pb[j][0] = transpose8x8(h2_bits(__floats2half2_rn(p[0], p[1])));
                 pb[j][1] = transpose8x8(h2_bits(__floats2half2_rn(p[2], p[3])));
             }
-            // V: channels kPer g + 0 .. kPer - 1 of the lane's four keys, two keys a pair
+            // V: channels kPer g .. + kPer - 1 of the lane's four keys, two keys a pair
             uint32_t va[kPer], vb[kPer];
-            const __half2 s01 = e4m3x2_to_half2((uint16_t)(x.vs[q] & 0xFFFFu));
-            const __half2 s23 = e4m3x2_to_half2((uint16_t)(x.vs[q] >> 16));
-            const __half2 by6 = bits_h2(kMulBits), by8 = bits_h2(kMulCvt);
-            decode_v_bits(x.v[q][0].x, x.v[q][1].x, __hmul2(s01, by6), va);
-            decode_v_bits(x.v[q][2].x, x.v[q][3].x, __hmul2(s23, by6), vb);
-            if (D == 128) {
-                decode_v_cvt(x.v[q][0].y, x.v[q][1].y, __hmul2(s01, by8), va + 8);
-                decode_v_cvt(x.v[q][2].y, x.v[q][3].y, __hmul2(s23, by8), vb + 8);
+            const __half2 s01 = e4m3x2_to_half2((uint16_t)(x.vs[q][0] | (x.vs[q][1] << 8)));
+            const __half2 s23 = e4m3x2_to_half2((uint16_t)(x.vs[q][2] | (x.vs[q][3] << 8)));
+#pragma unroll
+            for (int e = 0; e < D / 64; e++) {
+                decode8_rows(x.v[q][0][e], x.v[q][1][e], s01, va + 8 * e);
+                decode8_rows(x.v[q][2][e], x.v[q][3][e], s23, vb + 8 * e);
             }
 #pragma unroll
             for (int j = 0; j < NT; j++)
@@ -437,7 +488,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const __grid_consta
             float sum = l[j][e];
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-            if (g == 0) sml[warp][8 * j + 2 * t + e] = make_float2(m[j][e], sum);
+            if (g == 0) sml[warp][8 * j + 2 * t + e] = make_float2(limit[j][e] == kLazy ? -nm[j][e] : kFloor, sum);
 #pragma unroll
             for (int r = 0; r < kSteps; r++) {
                 so[warp][8 * j + 2 * t + e][kPer * g + 2 * r] = o[j][r][e];
@@ -445,7 +496,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_kernel(const __grid_consta
             }
         }
     __syncthreads();
-    const float back = __ldg(v.a32[1]) * kDecodeBack;
+    const float back = __ldg(v.a32[1]);
     for (int i = threadIdx.x; i < rows.n * (D / 2); i += kWarps * 32) {
         const int n = i / (D / 2), d = i % (D / 2) * 2;
         float mx = sml[0][n].x;
@@ -506,7 +557,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
             y[2 * e + 1] += x.y * wgt;
         }
     }
-    const float f2 = sum > 0.0f ? __fdiv_rn(__ldg(v.a32[1]) * kDecodeBack, sum) : 0.0f;
+    const float f2 = sum > 0.0f ? __fdiv_rn(__ldg(v.a32[1]), sum) : 0.0f;
     __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + (row * a.ld_o + (int64_t)qh * D) * 2);
 #pragma unroll
     for (int e = 0; e < D / 64; e++) dst[32 * e + lane] = __floats2bfloat162_rn(y[2 * e] * f2, y[2 * e + 1] * f2);
@@ -539,7 +590,7 @@ nvfp4_status check_paged(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, 
         return NVFP4_ERR_INVALID_ARG;
     if (c->head_dim != 64 && c->head_dim != 128) return NVFP4_ERR_UNSUPPORTED;
     if (c->page_size % kGroup != 0 || c->page_size > (1 << 20) || c->kv_heads > (1 << 16) || r->n_rows > (1 << 30) ||
-        r->max_len > (1 << 30))
+        r->max_len > (1 << 30) || (int64_t)c->n_pages * c->kv_heads > (((int64_t)1 << 32) - 1) / c->page_size)
         return NVFP4_ERR_UNSUPPORTED;
     if (r->n_seqs > 0 && r->n_rows > 0 && (!r->row_start || !r->lens || (r->max_pages > 0 && !r->pages)))
         return NVFP4_ERR_INVALID_ARG;
@@ -563,6 +614,9 @@ View make_view(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, void* ws) 
     v.pages = r->pages;
     v.n_pages = c->n_pages;
     v.page_size = c->page_size;
+    v.page_shift = -1;
+    for (int i = 0; i < 31; i++)
+        if (c->page_size == 1 << i) v.page_shift = i;
     v.kv_heads = c->kv_heads;
     v.d = c->head_dim;
     v.n_seqs = r->n_seqs;

@@ -18,6 +18,7 @@ struct View {
     const int32_t* lens;
     const int32_t* pages;
     int n_pages, page_size, kv_heads, d;
+    int page_shift;  // page_size = 2^page_shift, or -1
     int n_seqs, max_pages, n_rows;
     DevError* err;
 };

@@ -11,10 +11,7 @@
 //   warp 16     one thread issuing the tcgen05 products and their commits.
 // The decoding is what the tensor cores wait for most: a unit pays 2 * 128 * d
 // elements of it for 4 * 256 * 128 * d operations, and one warp a scheduler
-// cannot issue it fast enough, hence eight producer warps.  Half of it uses the
-// conversion unit (K) and half shifts and masks (V; fp4mma.cuh), whose pairs
-// are four channels apart: V's channels, and with them O's, lie in the order
-// 0 4 1 5 2 6 3 7 of every eight.
+// cannot issue it fast enough, hence eight producer warps.
 // Registers: 640 threads start with 96 each; the producers give 32 of theirs to
 // the softmax (setmaxnreg).
 // Shared memory: Q_A, Q_B, K, V[2], P_A, P_B, each of 8 x 8 core matrices
@@ -162,18 +159,16 @@ __device__ __forceinline__ void fetch(const AttnArgs& a, const Unit& w, int i, i
     }
 }
 
-// K: e2m1 s in the channels' order; V: 2^-8 e2m1 s in the order above.
-template <int D, bool V>
+// Its values e2m1 s (exact in binary16) into the operand at `base`.
+template <int D>
 __device__ __forceinline__ void store_half(const HalfRow<D>& h, uint32_t base, int row, int half) {
 #pragma unroll
     for (int w = 0; w < D / 16; w++) {  // 8 channels each
         const uint4& q = h.c[w / 4];
         const uint32_t c = (w & 3) == 0 ? q.x : (w & 3) == 1 ? q.y : (w & 3) == 2 ? q.z : q.w;
         const __half2 two = e4m3x2_to_half2((uint16_t)(h.sc >> (16 * (w / 4))));
-        const __half2 s = ((w / 2) & 1) ? __high2half2(two) : __low2half2(two);
         uint32_t o[4];
-        if (V) decode8_bits(c, __hmul2(s, bits_h2(kMulBits)), o);
-        else decode8_cvt(c, s, o);
+        decode8(c, ((w / 2) & 1) ? __high2half2(two) : __low2half2(two), o);
         st_shared16(base + (half * (D / 16) + w) * 2048 + row * 16, make_uint4(o[0], o[1], o[2], o[3]));
     }
 }
@@ -193,12 +188,12 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, Shared& sh, uin
             // a buffer's first fill passes at once (parity 1 of a fresh barrier)
             if (!wait_or_stop(&sh.k_empty, ph_k ^ 1u, sh, a, 4)) return;
             ph_k ^= 1u;
-            store_half<D, false>(x.k, smem0 + Smem<D>::k, row, half);
+            store_half<D>(x.k, smem0 + Smem<D>::k, row, half);
             fence_proxy_async_smem();
             mbar_arrive(&sh.k_full);
             const uint32_t vb = nv & 1u;
             if (!wait_or_stop(&sh.v_empty[vb], ((nv >> 1) & 1u) ^ 1u, sh, a, 5)) return;
-            store_half<D, true>(x.v, smem0 + Smem<D>::v + vb * Smem<D>::kOperand, row, half);
+            store_half<D>(x.v, smem0 + Smem<D>::v + vb * Smem<D>::kOperand, row, half);
             fence_proxy_async_smem();
             mbar_arrive(&sh.v_full[vb]);
             nv++;
@@ -209,8 +204,7 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, Shared& sh, uin
 
 // ---- softmax ---------------------------------------------------------------
 // Pair f of the unit's sequence into Q at row `row` (zeros past the last),
-// scaled by 2^k so that its largest magnitude lies in [2^14, 2^15), as
-// binary16 (exact for values down to 2^-28 of it); returns 2^-k.
+// scaled by 2^k to binary16 (fp4mma.cuh); returns 2^-k.
 template <int D>
 __device__ __forceinline__ float load_q_row(const AttnArgs& a, const Unit& w, uint32_t q_s, int f, int row) {
     uint4 v[D / 8];
@@ -223,23 +217,14 @@ __device__ __forceinline__ float load_q_row(const AttnArgs& a, const Unit& w, ui
 #pragma unroll
         for (int c = 0; c < D / 8; c++) v[c] = make_uint4(0u, 0u, 0u, 0u);
     }
-    uint32_t mx = 0u;
-#pragma unroll
-    for (int c = 0; c < D / 8; c++)
-        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu),
-                                   __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu)));
-    mx = max(mx & 0xFFFFu, mx >> 16);
-    const int k = mx == 0u ? 0 : min(126, 141 - (int)(mx >> 7));
-    const float pk = __uint_as_float((uint32_t)(127 + k) << 23);
+    const RowScale rs = row_scale(max_bits<D / 8>(v));
 #pragma unroll
     for (int c = 0; c < D / 8; c++) {
-        uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            x[e] = h2_bits(__floats2half2_rn(__uint_as_float(x[e] << 16) * pk, __uint_as_float(x[e] & 0xFFFF0000u) * pk));
+        uint32_t x[4];
+        scale8(v[c], rs.up, x);
         st_shared16(q_s + c * 2048 + row * 16, make_uint4(x[0], x[1], x[2], x[3]));
     }
-    return __uint_as_float((uint32_t)(127 - k) << 23);
+    return rs.down;
 }
 
 // What a row sees of a tile: keys below `hi` that are at least `lo` or below
@@ -310,7 +295,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
     const uint32_t lane_off = (uint32_t)(row & ~31) << 16;
     const uint32_t t_s = tmem + kSCol + 128 * X + lane_off, t_o = tmem + kOCol + 128 * X + lane_off;
     const uint32_t q_s = smem0 + Smem<D>::q + X * Smem<D>::kOperand, p_s = smem0 + Smem<D>::p + X * Smem<D>::kP;
-    const float ck = __ldg(a.v.a32[0]) * a.scale_log2, back = __ldg(a.v.a32[1]) * kDecodeBack;
+    const float ck = __ldg(a.v.a32[0]) * a.scale_log2, back = __ldg(a.v.a32[1]);
     uint32_t ph_s = 0u, ph_o = 0u;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const Unit w = get_unit(a, (int)u);
@@ -393,15 +378,12 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
                 for (int j = 0; j < 32; j++) r[j] = 0u;
             }
             if (!real) continue;
-            // channels 8 g + 0 .. 7 lie at positions 0 2 4 6 1 3 5 7 of their eight
             if (a.splits > 1) {
                 float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + 32 * c);
 #pragma unroll
-                for (int g = 0; g < 4; g++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++)
-                        dst[2 * g + h] = make_float4(__uint_as_float(r[8 * g + h]), __uint_as_float(r[8 * g + h + 2]),
-                                                     __uint_as_float(r[8 * g + h + 4]), __uint_as_float(r[8 * g + h + 6]));
+                for (int g = 0; g < 8; g++)
+                    dst[g] = make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
+                                         __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
             } else {
                 uint4* dst = reinterpret_cast<uint4*>(a.o + (orow * a.ld_o + (int64_t)qh * D + 32 * c) * 2);
 #pragma unroll
@@ -409,9 +391,8 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
                     uint32_t x[4];
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
-                        const int j = 8 * g + (e & 1) * 4 + (e >> 1);
-                        const __nv_bfloat162 b =
-                            __floats2bfloat162_rn(__uint_as_float(r[j]) * inv_l, __uint_as_float(r[j + 2]) * inv_l);
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[8 * g + 2 * e]) * inv_l,
+                                                                       __uint_as_float(r[8 * g + 2 * e + 1]) * inv_l);
                         x[e] = *reinterpret_cast<const uint32_t*>(&b);
                     }
                     dst[g] = make_uint4(x[0], x[1], x[2], x[3]);

@@ -402,7 +402,8 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const int32_t* slot
  * Row (p * kv_heads + h) * page_size + o is token o of page p, head h: its
  * head_dim / 2 code bytes at that multiple in *_codes, its head_dim / 16 scale
  * bytes in *_scales.  head_dim 64 or 128, page_size a multiple of 16 up to
- * 2^20, kv_heads up to 2^16 (else NVFP4_ERR_UNSUPPORTED). */
+ * 2^20, kv_heads up to 2^16, fewer than 2^32 rows (else
+ * NVFP4_ERR_UNSUPPORTED). */
 typedef struct {
     void* k_codes;
     void* k_scales;
