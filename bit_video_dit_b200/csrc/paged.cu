@@ -153,15 +153,17 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
 // group) and a run of 32-key tiles; 4 warps take the tiles in turn, each with
 // its own running maximum and sum.  Both products have the cache as the A
 // operand (S^T = K Q^T, O^T = V^T P^T), so eight rows fill a matrix
-// instruction's columns; a lane's loads are whole 16-byte (K) and 8-byte (V)
-// pieces of rows, with the contraction's columns permuted to fit, and P^T comes
-// from S^T by an 8 x 8 transpose in registers.
+// instruction's columns; a lane reads whole 16-byte (K) and 8-byte (V) pieces of
+// rows, with the contraction's columns permuted to fit, and P^T comes from S^T
+// by an 8 x 8 transpose in registers.  The cache's bytes pass through a ring of
+// tiles in shared memory a warp, so that no registers wait for them.
 //
 // Bound: the cache's bytes (a key and value are 9/8 head_dim bytes a head),
 // and beside them the decoding (fp4mma.cuh).  Long sequences are split over
 // CTAs and joined by combine_kernel.
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 32;  // keys of a tile
+constexpr int kSms = 148;
 constexpr int kWarps = 4;
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -178,93 +180,85 @@ __device__ __forceinline__ int group_page(const View& v, const int32_t* table, c
     return i < v.max_pages ? __ldg(table + i) : -2;
 }
 
-// One lane's share of a 32-key tile.
+// A warp's ring of 32-key tiles in shared memory, filled by asynchronous
+// copies: the tile's K codes, V codes, K scales, V scales.  D = 128: the two
+// halves of a V row change places in every other pair of keys, which spreads
+// the reads below over all banks.
 template <int D>
-struct KVTile {
-    uint32_t k[2][2][D / 32];  // keys 16 q + g, + 8: the codes of channels D / 4 t ..
-    uint32_t ks[2][2];         // their scales: two blocks (D = 64: one, twice) in bits 15:0
-    uint32_t v[2][4][D / 64];  // keys 16 q + 2 t + {0, 1, 8, 9}: the codes of channels D / 8 g ..
-    uint32_t vs[2][4];         // their scale
-    bool ok[2];                // the 16 keys lie in a page of the cache
+struct Ring {
+    static constexpr int kStages = 4;
+    static constexpr int kCodes = kKeys * D / 2, kScales = kKeys * D / 16;
+    static constexpr int k = 0, v = kCodes, ks = 2 * kCodes, vs = 2 * kCodes + kScales;
+    static constexpr int bytes = 2 * (kCodes + kScales);
 };
 
-template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
-    if (N == 4) {
-        const uint4 x = ld_stream16(p);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    } else if (N == 2) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-        w[0] = x.x, w[1] = x.y;
-    } else {
-        w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-    }
+// 16 bytes to shared memory, those behind the first `n` as zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
-// The lane's places in the cache for one head: add row * (D / 2) to a codes
-// pointer, row * (D / 16) to a scales pointer.
-struct Lane {
-    const uint8_t *kc, *ks, *vc, *vs;
-    uint32_t page_rows, head_row;  // rows of a page over all heads, of the heads before this one
-};
-
+// Tile at key k0 into a ring slot.  Groups that no row sees, and what lies
+// behind the last key (it is not a value), become zeros.
 template <int D>
-__device__ __forceinline__ void load_tile(const View& v, const Lane& ln, int b, const Span& sp, int k0, int t,
-                                          const int* pages, KVTile<D>& x) {
+__device__ __forceinline__ void load_tile(const View& v, int b, uint32_t head_row, const Span& sp, int k0, int lane,
+                                          const int* pages, uint32_t dst) {
+    constexpr int kChunks = D / 32;            // of a row of codes
+    constexpr int kRows = 32 / kChunks;        // rows that the warp copies at a time
+    constexpr int kScaleChunks = kKeys * D / 256;
+    const uint32_t page_rows = (uint32_t)v.kv_heads * (uint32_t)v.page_size;
+    uint32_t row[2];
+    bool ok[2];
 #pragma unroll
     for (int q = 0; q < 2; q++) {
         const int kq = k0 + 16 * q;
-        x.ok[q] = (unsigned)pages[q] < (unsigned)v.n_pages;
-        if (x.ok[q]) {
-            const int at = v.page_shift >= 0 ? kq & (v.page_size - 1) : kq % v.page_size;
-            const uint32_t row = (uint32_t)pages[q] * ln.page_rows + ln.head_row + (uint32_t)at;  // below 2^32 (host)
-            const uint8_t* kc = ln.kc + (uint64_t)row * (D / 2);
-            const uint8_t* vc = ln.vc + (uint64_t)row * (D / 2);
-            const uint8_t* ks = ln.ks + (uint64_t)row * (D / 16);
-            const uint8_t* vs = ln.vs + (uint64_t)row * (D / 16);
+        ok[q] = (unsigned)pages[q] < (unsigned)v.n_pages;
+        if (!ok[q] && pages[q] != -1) record_error(v.err, NVFP4_ERR_DEVICE, (uint32_t)b);
+        const int at = v.page_shift >= 0 ? kq & (v.page_size - 1) : kq % v.page_size;
+        row[q] = ok[q] ? (uint32_t)pages[q] * page_rows + head_row + (uint32_t)at : 0u;  // below 2^32 (host)
+    }
+    const int r0 = lane / kChunks, c = lane % kChunks;
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                load_words<D / 32>(kc + 8 * h * (D / 2), x.k[q][h]);
-                if (D == 128) x.ks[q][h] = __ldg(reinterpret_cast<const uint16_t*>(ks + 8 * h * 8));
-                else x.ks[q][h] = __ldg(ks + 8 * h * 4) * 0x101u;
-            }
-            if (kq + kGroup <= sp.hi) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int key = (i & 1) + 8 * (i >> 1);  // + 2 t
-                    load_words<D / 64>(vc + key * (D / 2), x.v[q][i]);
-                    x.vs[q][i] = __ldg(vs + key * (D / 16));
-                }
-            } else {  // what lies behind the last key is not a value
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int key = (i & 1) + 8 * (i >> 1);
-                    x.vs[q][i] = 0u;
-#pragma unroll
-                    for (int e = 0; e < D / 64; e++) x.v[q][i][e] = 0u;
-                    if (kq + 2 * t + key < sp.hi) {
-                        load_words<D / 64>(vc + key * (D / 2), x.v[q][i]);
-                        x.vs[q][i] = __ldg(vs + key * (D / 16));
-                    }
-                }
-            }
-        } else {
-            if (pages[q] != -1) record_error(v.err, NVFP4_ERR_DEVICE, (uint32_t)b);
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                x.ks[q][h] = 0u;
-#pragma unroll
-                for (int e = 0; e < D / 32; e++) x.k[q][h][e] = 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                x.vs[q][i] = 0u;
-#pragma unroll
-                for (int e = 0; e < D / 64; e++) x.v[q][i][e] = 0u;
-            }
-        }
+    for (int j = 0; j < kKeys / kRows; j++) {
+        const int key = j * kRows + r0, q = j * kRows / 16;
+        const uint64_t off = (uint64_t)(row[q] + (uint32_t)(key - 16 * q)) * (D / 2) + 16 * c;
+        const int n = ok[q] && k0 + key < sp.hi ? 16 : 0;
+        const int cv = D == 128 ? c ^ (key & 2) : c;
+        copy16(dst + Ring<D>::k + key * (D / 2) + 16 * c, v.codes[0] + off, n);
+        copy16(dst + Ring<D>::v + key * (D / 2) + 16 * cv, v.codes[1] + off, n);
+    }
+    if (lane < 2 * kScaleChunks) {
+        const int t = lane / kScaleChunks, i = lane % kScaleChunks;  // K or V, its chunk
+        const int key = i * (256 / D);
+        const uint64_t off = (uint64_t)((key < 16 ? row[0] : row[1] - 16u) + (uint32_t)key) * (D / 16);
+        const int n = (key < 16 ? ok[0] : ok[1]) ? min(16, max(0, sp.hi - k0 - key) * (D / 16)) : 0;
+        copy16(dst + (t ? Ring<D>::vs : Ring<D>::ks) + 16 * i, v.scales[t] + off, n);
     }
 }
+
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t p, uint32_t* w) {
+    if (N == 4)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(p));
+    else if (N == 2)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
+    else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p));
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t p) {
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(p));
+    return x;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t p) {
+    uint32_t x;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(p));
+    return x;
+}
+
+// Which of a group's 16 keys is row r < 8 of the S product (row r + 8: 8 more):
+// the transpose hands rows 2 t and 2 t + 1 to lane t, whose V rows then are
+// keys t, 4 + (t ^ 1), and 8 more, in four different bank quarters each time.
+__device__ __forceinline__ int key_of_row(int r) { return (r & 1) ? 4 + ((r >> 1) ^ 1) : r >> 1; }
 
 // One key's D / 4 codes and their scales -> D / 8 pairs
 template <int D>
@@ -275,53 +269,52 @@ __device__ __forceinline__ void decode_k(const uint32_t* c, uint32_t sc, uint32_
     for (int w = 0; w < D / 32; w++) decode8(c[w], w < D / 64 ? s0 : s1, o + 4 * w);
 }
 
+template <int D>
+constexpr int decode_smem() {
+    // (the join's buffers, 16 columns at most, are smaller)
+    static_assert(kWarps * 16 * ((D + 4) * 4 + 8) <= kWarps * Ring<D>::kStages * Ring<D>::bytes, "join");
+    return kWarps * Ring<D>::kStages * Ring<D>::bytes;
+}
+
+// CTAs of a launch: three an SM (two with 16 columns) by registers and shared memory.
+template <int NT>
+constexpr int decode_ctas() {
+    return kSms * (NT == 1 ? 3 : 2);
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(const __grid_constant__ AttnArgs a) {
+__device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, uint8_t* ring_mem) {
     constexpr int kCols = 8 * NT, kSteps = D / 16, kPer = D / 8;  // kPer: a lane's channels of O
-    __shared__ float so[kWarps][kCols][D + 4];
-    __shared__ float2 sml[kWarps][kCols];
     const View& v = a.v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    unsigned u = blockIdx.x;
-    const int split = (int)(u % (unsigned)a.splits);
-    u /= (unsigned)a.splits;
-    const int rt = (int)(u % (unsigned)a.row_tiles);
-    u /= (unsigned)a.row_tiles;
-    const int head = (int)(u % (unsigned)v.kv_heads), b = (int)(u / (unsigned)v.kv_heads);
-    const Seq s = load_seq(v, b);
-    if (s.n > a.max_rows) {  // more rows than the launch was sized for
-        record_error(v.err, NVFP4_ERR_DEVICE, (uint32_t)b);
-        return;
-    }
-    const int f0 = rt * kCols;
-    const Rows rows = unit_rows(a, s, f0, kCols);
-    if (rows.n == 0) return;
+    const Seq& s = u.s;
+    const Rows& rows = u.rows;
+    const int b = u.b, head = u.head, f0 = u.f0, begin = u.begin, end = u.end;
     const Tiles<kKeys> tiles(rows.span);
-    const int per = tiles_per_split(a, tiles.count);
-    const int begin = split * per, end = min(tiles.count, begin + per);
-    if (split > 0 && begin >= end) return;
 
-    Lane ln;
-    ln.kc = v.codes[0] + g * (D / 2) + D / 8 * t;
-    ln.ks = v.scales[0] + g * (D / 16) + D / 64 * t;
-    ln.vc = v.codes[1] + 2 * t * (D / 2) + D / 16 * g;
-    ln.vs = v.scales[1] + 2 * t * (D / 16) + (D == 128 ? g : g / 2);
-    ln.page_rows = (uint32_t)v.kv_heads * (uint32_t)v.page_size;
-    ln.head_row = (uint32_t)head * (uint32_t)v.page_size;
+    const uint32_t ring = smem_u32(ring_mem) + (uint32_t)(warp * Ring<D>::kStages * Ring<D>::bytes);
+    const uint32_t head_row = (uint32_t)head * (uint32_t)v.page_size;
     const int32_t* table = v.pages + (int64_t)b * v.max_pages;
 
-    // pages are looked up two tiles ahead, their data loaded one tile ahead
-    KVTile<D> x;
-    int pages[2] = {-1, -1};
-    if (begin + warp < end) {
-        const int k0 = tiles.key0(begin + warp);
-        const int first[2] = {group_page(v, table, rows.span, k0), group_page(v, table, rows.span, k0 + 16)};
-        load_tile<D>(v, ln, b, rows.span, k0, t, first, x);
-        if (begin + warp + kWarps < end) {
-            const int k1 = tiles.key0(begin + warp + kWarps);
-            pages[0] = group_page(v, table, rows.span, k1);
-            pages[1] = group_page(v, table, rows.span, k1 + 16);
+    // the warp's tiles begin + warp, + kWarps, ..: copies run kStages - 1 tiles ahead, page lookups one more
+    int pages[2];
+    auto lookup = [&](int i) {
+        if (i < end) {
+            const int k0 = tiles.key0(i);
+            pages[0] = group_page(v, table, rows.span, k0);
+            pages[1] = group_page(v, table, rows.span, k0 + 16);
         }
+    };
+    auto fetch = [&](int i, int slot) {
+        if (i < end)
+            load_tile<D>(v, b, head_row, rows.span, tiles.key0(i), lane, pages, ring + (uint32_t)(slot * Ring<D>::bytes));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    lookup(begin + warp);
+#pragma unroll
+    for (int i = 0; i < Ring<D>::kStages - 1; i++) {
+        fetch(begin + warp + i * kWarps, i);
+        lookup(begin + warp + (i + 1) * kWarps);
     }
 
     // queries: column n of tile j is row f0 + 8 j + n; columns past the last row are zeros and nobody reads them
@@ -359,25 +352,34 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(co
             for (int e = 0; e < 4; e++) o[j][i][e] = 0.0f;
     }
 
-#pragma unroll 2
+    // the lane's places in a ring slot
+    const int kr = key_of_row(g);
+    const uint32_t l_k = Ring<D>::k + kr * (D / 2) + D / 8 * t, l_ks = Ring<D>::ks + kr * (D / 16) + D / 64 * t;
+    const int v0 = t, v1 = 4 + (t ^ 1);  // keys of a group whose V rows the lane decodes, and 8 more
+    const uint32_t l_v0 = Ring<D>::v + v0 * (D / 2) + (D == 128 ? 16 * ((g >> 1) ^ (v0 & 2)) + 8 * (g & 1) : 4 * g);
+    const uint32_t l_v1 = Ring<D>::v + v1 * (D / 2) + (D == 128 ? 16 * ((g >> 1) ^ (v1 & 2)) + 8 * (g & 1) : 4 * g);
+    const uint32_t l_vs = Ring<D>::vs + (D == 128 ? g : g / 2);
+    int slot = 0;
+
+#pragma unroll 1
     for (int i = begin + warp; i < end; i += kWarps) {
         const int k0 = tiles.key0(i);
-        KVTile<D> next;
-        if (i + kWarps < end) {
-            load_tile<D>(v, ln, b, rows.span, tiles.key0(i + kWarps), t, pages, next);
-            if (i + 2 * kWarps < end) {
-                const int k2 = tiles.key0(i + 2 * kWarps);
-                pages[0] = group_page(v, table, rows.span, k2);
-                pages[1] = group_page(v, table, rows.span, k2 + 16);
-            }
-        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(Ring<D>::kStages - 2) : "memory");
+        __syncwarp();  // the tile is there for every lane, and every lane has left the slot that is filled next
+        fetch(i + (Ring<D>::kStages - 1) * kWarps, (slot + Ring<D>::kStages - 1) % Ring<D>::kStages);
+        lookup(i + Ring<D>::kStages * kWarps);
+        const uint32_t at = ring + (uint32_t)(slot * Ring<D>::bytes);
+        slot = (slot + 1) % Ring<D>::kStages;
         // z: the scores' exponents, relative to the reference: 2^z is the weight
         float z[2][NT][4];
 #pragma unroll
         for (int q = 0; q < 2; q++) {
-            uint32_t ka[D / 8], kb[D / 8];
-            decode_k<D>(x.k[q][0], x.ks[q][0], ka);
-            decode_k<D>(x.k[q][1], x.ks[q][1], kb);
+            uint32_t ka[D / 8], kb[D / 8], w[D / 32];
+            const uint32_t k16 = at + l_k + 16 * q * (D / 2), s16 = at + l_ks + 16 * q * (D / 16);
+            lds_words<D / 32>(k16, w);
+            decode_k<D>(w, D == 128 ? lds_u16(s16) : lds_u8(s16) * 0x101u, ka);
+            lds_words<D / 32>(k16 + 8 * (D / 2), w);
+            decode_k<D>(w, D == 128 ? lds_u16(s16 + 8 * (D / 16)) : lds_u8(s16 + 8 * (D / 16)) * 0x101u, kb);
 #pragma unroll
             for (int j = 0; j < NT; j++) {
 #pragma unroll
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(co
 #pragma unroll
                 for (int e = 0; e < 4; e++) z[q][j][e] = fmaf(z[q][j][e], c_col[j][e & 1], nm[j][e & 1]);
         // every key of the tile seen by every row, or else key by key
-        const bool all = x.ok[0] && x.ok[1] && k0 + kKeys - 1 <= p_first &&
+        const bool all = k0 + kKeys - 1 <= p_first &&
                          (a.window == 0 || k0 > p_last - a.window || k0 + kKeys <= a.sinks);
         if (!all) {
 #pragma unroll
@@ -407,8 +409,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(co
                     for (int q = 0; q < 2; q++)
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            const int key = k0 + 16 * q + g + 8 * h;
-                            if (!(x.ok[q] && key <= p && (key >= lo || key < a.sinks))) z[q][j][2 * h + e] = -INFINITY;
+                            const int key = k0 + 16 * q + kr + 8 * h;
+                            if (!(key <= p && (key >= lo || key < a.sinks))) z[q][j][2 * h + e] = -INFINITY;
                         }
                 }
         }
@@ -464,12 +466,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(co
             }
             // V: channels kPer g .. + kPer - 1 of the lane's four keys, two keys a pair
             uint32_t va[kPer], vb[kPer];
-            const __half2 s01 = e4m3x2_to_half2((uint16_t)(x.vs[q][0] | (x.vs[q][1] << 8)));
-            const __half2 s23 = e4m3x2_to_half2((uint16_t)(x.vs[q][2] | (x.vs[q][3] << 8)));
 #pragma unroll
-            for (int e = 0; e < D / 64; e++) {
-                decode8_rows(x.v[q][0][e], x.v[q][1][e], s01, va + 8 * e);
-                decode8_rows(x.v[q][2][e], x.v[q][3][e], s23, vb + 8 * e);
+            for (int h = 0; h < 2; h++) {
+                uint32_t w0[D / 64], w1[D / 64];
+                const uint32_t key = 16 * q + 8 * h;
+                lds_words<D / 64>(at + l_v0 + key * (D / 2), w0);
+                lds_words<D / 64>(at + l_v1 + key * (D / 2), w1);
+                const __half2 two = e4m3x2_to_half2((uint16_t)(lds_u8(at + l_vs + (key + v0) * (D / 16)) |
+                                                               (lds_u8(at + l_vs + (key + v1) * (D / 16)) << 8)));
+#pragma unroll
+                for (int e = 0; e < D / 64; e++) decode8_rows(w0[e], w1[e], two, (h ? vb : va) + 8 * e);
             }
 #pragma unroll
             for (int j = 0; j < NT; j++)
@@ -477,10 +483,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(co
                 for (int r = 0; r < kSteps; r++)
                     mma_16816(o[j][r], va[2 * r], va[2 * r + 1], vb[2 * r], vb[2 * r + 1], pb[j][0], pb[j][1]);
         }
-        x = next;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the ring's memory is the join's from here on
 
     // join the four warps
+    float(*so)[kCols][D + 4] = reinterpret_cast<float(*)[kCols][D + 4]>(ring_mem);
+    float2(*sml)[kCols] = reinterpret_cast<float2(*)[kCols]>(ring_mem + kWarps * kCols * (D + 4) * 4);
 #pragma unroll
     for (int j = 0; j < NT; j++)
 #pragma unroll
@@ -510,55 +519,69 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(co
             y0 += so[w][n][d] * f;
             y1 += so[w][n][d + 1] * f;
         }
-        const int row = s.first + (f0 + n) / a.group, qh = head * a.group + (f0 + n) % a.group;
-        if (a.splits > 1) {
-            const int64_t slot = ((int64_t)split * v.n_rows + row) * a.heads + qh;
-            *reinterpret_cast<float2*>(a.part_o + slot * D + d) = make_float2(y0, y1);
-            if (d == 0) a.part_ml[slot] = make_float2(mx, sum);
+        if (u.slot >= 0) {
+            const int64_t at = (int64_t)u.slot * kCols + n;
+            *reinterpret_cast<float2*>(a.part_o + at * D + d) = make_float2(y0, y1);
+            if (d == 0) a.part_ml[at] = make_float2(mx, sum);
         } else {
+            const int row = s.first + (f0 + n) / a.group, qh = head * a.group + (f0 + n) % a.group;
             const float f = sum > 0.0f ? __fdiv_rn(back, sum) : 0.0f;  // a row that sees no key: zeros
             *reinterpret_cast<__nv_bfloat162*>(a.o + ((int64_t)row * a.ld_o + (int64_t)qh * D + d) * 2) =
                 __floats2bfloat162_rn(y0 * f, y1 * f);
         }
     }
+    __syncthreads();  // the next piece fills the ring again
 }
 
-// A warp joins the splits of one (row, query head).  `cols` and T: the rows of
-// a unit and the keys of a tile in the kernel that wrote the parts.
-template <int D, int T>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ AttnArgs a, int cols) {
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(const __grid_constant__ AttnArgs a) {
+    extern __shared__ __align__(128) uint8_t ring_mem[];
+    __shared__ RunScratch scratch;
+    // no run shorter than a tile a warp
+    Run run = make_run<8 * NT, kKeys, kWarps * 32>(a, kWarps, scratch);
+    Piece u;
+    int4 cut = make_int4(0, 0, 0, 0);
+    while (next_piece<8 * NT, kKeys>(a, run, u)) {
+        decode_piece<D, NT>(a, u, ring_mem);
+        if (u.pieces) cut = make_int4(u.pieces, u.pair, u.head, 0);
+    }
+    if (threadIdx.x == 0) a.cut[blockIdx.x] = cut;
+}
+
+// Joins the pieces of the unit that CTA blockIdx.x began, a warp a row.
+template <int D, int COLS>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnArgs a) {
     const View& v = a.v;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const int64_t each = (int64_t)a.max_rows * a.heads;
-    const int b = (int)(w / each), i = (int)(w % each) / a.heads, qh = (int)(w % each) % a.heads;
-    if (b >= v.n_seqs) return;
-    const Seq s = load_seq(v, b);
-    if (s.n > a.max_rows || i >= s.n) return;
-    const int f = i * a.group + qh % a.group;
-    const Rows rows = unit_rows(a, s, f / cols * cols, cols);
-    const Tiles<T> tiles(rows.span);
-    const int per = tiles_per_split(a, tiles.count);
-    const int parts = max(1, (tiles.count + per - 1) / per);
-    const int64_t row = s.first + i;
+    const int4 cut = __ldcg(a.cut + blockIdx.x);
+    const int lane = threadIdx.x & 31, n = (int)blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (cut.x == 0) return;
+    const Seq s = load_seq(v, cut.y / a.row_tiles);
+    const int f = cut.y % a.row_tiles * COLS + n;
+    if (n >= COLS || f >= s.n * a.group) return;
+    // piece 0 is the end of this CTA's run, piece p the beginning of CTA p later
+    auto at = [&](int p) { return (int64_t)(2 * ((int)blockIdx.x + p) + (p == 0)) * COLS + n; };
     float mx = kFloor, sum = 0.0f, y[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; e++) y[e] = 0.0f;
-    for (int p = 0; p < parts; p++) mx = fmaxf(mx, __ldcg(&a.part_ml[((int64_t)p * v.n_rows + row) * a.heads + qh].x));
-    for (int p = 0; p < parts; p++) {
-        const int64_t slot = ((int64_t)p * v.n_rows + row) * a.heads + qh;
-        const float2 ml = __ldcg(a.part_ml + slot);
-        const float wgt = ex2(ml.x - mx);
-        sum += ml.y * wgt;
+    for (int p = lane; p < cut.x; p += 32) mx = fmaxf(mx, __ldcg(&a.part_ml[at(p)].x));
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+#pragma unroll 4
+    for (int p = 0; p < cut.x; p++) {
+        const int64_t k = at(p);
+        const float2 ml = __ldcg(a.part_ml + k);
+        const float w = ex2(ml.x - mx);
+        sum += ml.y * w;
 #pragma unroll
         for (int e = 0; e < D / 64; e++) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(a.part_o + slot * D) + 32 * e + lane);
-            y[2 * e] += x.x * wgt;
-            y[2 * e + 1] += x.y * wgt;
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(a.part_o + k * D) + 32 * e + lane);
+            y[2 * e] += x.x * w;
+            y[2 * e + 1] += x.y * w;
         }
     }
     const float f2 = sum > 0.0f ? __fdiv_rn(__ldg(v.a32[1]), sum) : 0.0f;
-    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + (row * a.ld_o + (int64_t)qh * D) * 2);
+    const int64_t row = s.first + f / a.group, qh = cut.z * a.group + f % a.group;
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + (row * a.ld_o + qh * D) * 2);
 #pragma unroll
     for (int e = 0; e < D / 64; e++) dst[32 * e + lane] = __floats2bfloat162_rn(y[2 * e] * f2, y[2 * e + 1] * f2);
 }
@@ -574,7 +597,6 @@ using namespace nvfp4::paged;
 
 namespace {
 
-constexpr int kSms = 148;
 constexpr size_t kControl = 256;
 
 bool odd(const void* p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
@@ -654,13 +676,12 @@ nvfp4_status rows_call(bool append, const nvfp4_paged_cache* c, const nvfp4_page
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
-// How an attention call is cut up; the same for its workspace query.
+// How an attention call is launched; the same for its workspace query.
 struct Plan {
     bool chunks;  // chunk_kernel (paged_attention.cu), else decode_kernel
     int cols;     // (row, query head) pairs of a unit
-    int row_tiles, splits, split_tiles;
-    int64_t units;
-    size_t ws;
+    int row_tiles, ctas;
+    size_t cut, ml, o, ws;  // bytes from the workspace's start
 };
 
 bool make_plan(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, int heads, int window, int sinks, Plan* p) {
@@ -669,29 +690,19 @@ bool make_plan(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, int heads,
     // More pairs than the decode kernel's 16 columns would read (and decode) the keys several times
     p->chunks = pairs > 16;
     p->cols = p->chunks ? kChunkRows : pairs <= 8 ? 8 : 16;
-    const int keys = p->chunks ? kChunkKeys : kKeys;
-    const int64_t row_tiles = std::max<int64_t>(1, (pairs + p->cols - 1) / p->cols);
-    p->units = row_tiles * c->kv_heads * std::max(1, r->n_seqs);
-    if (p->units >= ((int64_t)1 << 31)) return false;
-    p->row_tiles = (int)row_tiles;
-    // the most tiles that one unit can see
-    const int64_t unit_rows = std::min<int64_t>(r->max_rows, p->cols);
+    p->row_tiles = (int)std::max<int64_t>(1, (pairs + p->cols - 1) / p->cols);
+    if ((int64_t)p->row_tiles * std::max(1, r->n_seqs) >= ((int64_t)1 << 31) - 1024) return false;
+    p->ctas = p->chunks ? kChunkCtas : p->cols == 8 ? decode_ctas<1>() : decode_ctas<2>();
+    // no more CTAs than the shortest runs of the most tiles
     int64_t seen = r->max_len;
-    if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + unit_rows + sinks + 2 * keys);
-    const int64_t most = (seen + keys - 1) / keys;
-    // runs of tiles such that about eight CTAs an SM have work, none shorter than a tile a warp; chunks: one CTA an
-    // SM, no run shorter than four tiles
-    const int64_t want = std::max<int64_t>(1, (int64_t)kSms * (p->chunks ? 1 : 8) / p->units);
-    int64_t per = std::max<int64_t>(kWarps, (most + want - 1) / want);
-    int64_t splits = std::max<int64_t>(1, (most + per - 1) / per);
-    if (p->units * splits >= ((int64_t)1 << 31)) return false;
-    p->splits = (int)splits;
-    p->split_tiles = (int)per;
-    p->ws = kControl;
-    if (splits > 1) {
-        const int64_t slots = splits * (int64_t)r->n_rows * heads;
-        p->ws += (size_t)(slots * c->head_dim * 4 + slots * 8);
-    }
+    if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + sinks + std::min<int64_t>(r->max_rows, p->cols));
+    const int keys = p->chunks ? kChunkKeys : kKeys, least = p->chunks ? kChunkLeast : kWarps;
+    const int64_t tiles = (seen / keys + 3) * p->row_tiles * std::max(1, r->n_seqs);  // ragged at both ends and the sinks'
+    p->ctas = (int)std::min<int64_t>(p->ctas, (tiles * c->kv_heads + least - 1) / least);
+    p->cut = kControl;
+    p->ml = p->cut + (size_t)p->ctas * sizeof(int4);
+    p->o = p->ml + (size_t)p->ctas * 2 * p->cols * sizeof(float2);
+    p->ws = p->o + (size_t)p->ctas * 2 * p->cols * c->head_dim * sizeof(float);
     return true;
 }
 
@@ -754,30 +765,41 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, co
     a.sinks = window > 0 ? sinks : 0;
     a.max_rows = rows->max_rows;
     a.row_tiles = p.row_tiles;
-    a.splits = p.splits;
-    a.split_tiles = p.split_tiles;
     const float sc = scale > 0.0f ? scale : 1.0f / sqrtf((float)cache->head_dim);
     a.scale_log2 = sc * 1.4426950408889634f;  // log2(e)
-    const int64_t slots = (int64_t)p.splits * rows->n_rows * heads;
-    a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kControl);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * cache->head_dim);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.cut = reinterpret_cast<int4*>(ws + p.cut);
+    a.part_ml = reinterpret_cast<float2*>(ws + p.ml);
+    a.part_o = reinterpret_cast<float*>(ws + p.o);
     if (p.chunks) {
-        st = launch_chunks(a, p.units * p.splits, (cudaStream_t)stream);
+        st = launch_chunks(a, (unsigned)p.ctas, (cudaStream_t)stream);
         if (st != NVFP4_OK) return st;
     } else {
         void (*kern)(AttnArgs) = cache->head_dim == 128 ? (p.cols == 8 ? decode_kernel<128, 1> : decode_kernel<128, 2>)
                                                         : (p.cols == 8 ? decode_kernel<64, 1> : decode_kernel<64, 2>);
-        kern<<<(unsigned)(p.units * p.splits), kWarps * 32, 0, (cudaStream_t)stream>>>(a);
+        static PerDevice<int> ready;
+        int done = 0;
+        st = ready.get(&done, [](int, int& v) {
+            v = 1;
+            return cudaFuncSetAttribute(decode_kernel<128, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        decode_smem<128>()) == cudaSuccess &&
+                           cudaFuncSetAttribute(decode_kernel<128, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                decode_smem<128>()) == cudaSuccess &&
+                           cudaFuncSetAttribute(decode_kernel<64, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                decode_smem<64>()) == cudaSuccess &&
+                           cudaFuncSetAttribute(decode_kernel<64, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                decode_smem<64>()) == cudaSuccess
+                       ? NVFP4_OK
+                       : NVFP4_ERR_CUDA;
+        });
+        if (st != NVFP4_OK) return st;
+        kern<<<(unsigned)p.ctas, kWarps * 32, cache->head_dim == 128 ? decode_smem<128>() : decode_smem<64>(),
+               (cudaStream_t)stream>>>(a);
     }
-    if (p.splits > 1) {
-        const int64_t warps = (int64_t)rows->n_seqs * rows->max_rows * heads;
-        const int64_t grid = (warps + 3) / 4;
-        if (grid >= ((int64_t)1 << 31)) return NVFP4_ERR_UNSUPPORTED;
-        void (*join)(AttnArgs, int) = p.chunks ? (cache->head_dim == 128 ? combine_kernel<128, kChunkKeys>
-                                                                         : combine_kernel<64, kChunkKeys>)
-                                               : (cache->head_dim == 128 ? combine_kernel<128, kKeys>
-                                                                         : combine_kernel<64, kKeys>);
-        join<<<(unsigned)grid, 128, 0, (cudaStream_t)stream>>>(a, p.cols);
-    }
+    void (*join)(AttnArgs) =
+        cache->head_dim == 128
+            ? (p.chunks ? combine_kernel<128, kChunkRows> : p.cols == 8 ? combine_kernel<128, 8> : combine_kernel<128, 16>)
+            : (p.chunks ? combine_kernel<64, kChunkRows> : p.cols == 8 ? combine_kernel<64, 8> : combine_kernel<64, 16>);
+    join<<<dim3((unsigned)p.ctas, (unsigned)(p.cols / 8)), 256, 0, (cudaStream_t)stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }

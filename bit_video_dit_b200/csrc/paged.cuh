@@ -109,10 +109,11 @@ struct AttnArgs {
     uint8_t* o;
     int64_t ld_q, ld_o;
     int heads, group, window, sinks, max_rows;
-    int row_tiles, splits, split_tiles;
+    int row_tiles;  // units of the most rows a sequence may have
     float scale_log2;
-    float* part_o;   // [splits][n_rows][heads][d]
-    float2* part_ml; // [splits][n_rows][heads] (reference maximum, sum)
+    int4* cut;        // [CTAs]: (pieces of the unit that the CTA begins and does not end, or 0; its pair, head)
+    float* part_o;    // [CTAs][2][cols][d] unnormalised
+    float2* part_ml;  // [CTAs][2][cols] (reference maximum, sum)
 };
 
 // Rows f0 .. f0 + cols - 1 of a sequence's n * group (row, query head) pairs.
@@ -134,15 +135,138 @@ __device__ __forceinline__ Rows unit_rows(const AttnArgs& a, const Seq& s, int f
     return r;
 }
 
-// Tiles of one split of a unit with `count` tiles.
-__device__ __forceinline__ int tiles_per_split(const AttnArgs& a, int count) {
-    return max(a.split_tiles, (count + a.splits - 1) / a.splits);
+// The work of a launch is one list of key tiles: for every pair of a sequence
+// and a run of its rows, for every K/V head, that unit's tiles.  The list is
+// cut into equal runs, one a CTA, whatever the lengths; a unit that lies in
+// several runs leaves a piece in each, which combine_kernel joins.  CTA k keeps
+// the piece of a unit that began before its run at 2 k, of one that ends after
+// it at 2 k + 1.
+struct Piece {
+    int b, head, f0;   // sequence, K/V head, first (row, query head) pair
+    int begin, end;    // tiles of the unit (a unit that sees none has one empty piece: 0, 0)
+    int slot;          // where the piece is kept, or -1 when it is the whole unit
+    int pair, pieces;  // of a unit that begins here and ends in a later run: its pieces
+    Seq s;
+    Rows rows;
+};
+
+struct Run {
+    int64_t x, end, base;  // the run's next tile and end, first tile of the pair
+    int pair, per;
+};
+
+// Tiles of pair j (0: no rows; a unit that sees no key counts as one tile).
+template <int COLS, int T>
+__device__ __forceinline__ int pair_tiles(const AttnArgs& a, int j, Seq* seq, Rows* rows, int* real) {
+    const int b = j / a.row_tiles;
+    *seq = load_seq(a.v, b);
+    if (seq->n > a.max_rows) {  // more rows than the launch was sized for
+        record_error(a.v.err, NVFP4_ERR_DEVICE, (uint32_t)b);
+        seq->n = 0;
+    }
+    *rows = unit_rows(a, *seq, j % a.row_tiles * COLS, COLS);
+    if (rows->n == 0) return 0;
+    const Tiles<T> tiles(rows->span);
+    *real = tiles.count;
+    return max(1, tiles.count);
+}
+
+struct RunScratch {
+    long long warp_sum[32];
+    long long base;
+    int pair;
+};
+
+// The CTA's run (all THREADS threads; none is shorter than `least` tiles).
+template <int COLS, int T, int THREADS>
+__device__ __forceinline__ Run make_run(const AttnArgs& a, int least, RunScratch& sh) {
+    const int pairs = a.v.n_seqs * a.row_tiles, each = (pairs + THREADS - 1) / THREADS;
+    const int j0 = min(pairs, (int)threadIdx.x * each), j1 = min(pairs, j0 + each);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Seq s;
+    Rows r;
+    int real;
+    long long sum = 0;
+    for (int j = j0; j < j1; j++) sum += pair_tiles<COLS, T>(a, j, &s, &r, &real);
+    long long incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    if (threadIdx.x == 0) sh.pair = pairs;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; w++) {
+        if (w < warp) before += sh.warp_sum[w];
+        total += sh.warp_sum[w];
+    }
+    total *= a.v.kv_heads;
+    Run run;
+    run.per = (int)max((long long)least, (total + gridDim.x - 1) / gridDim.x);
+    run.x = (int64_t)blockIdx.x * run.per;
+    run.end = min((int64_t)total, run.x + run.per);
+    long long base = (before + incl - sum) * a.v.kv_heads;
+    if (base <= run.x && run.x < base + sum * a.v.kv_heads) {
+        for (int j = j0; j < j1; j++) {
+            const long long n = (long long)pair_tiles<COLS, T>(a, j, &s, &r, &real) * a.v.kv_heads;
+            if (run.x < base + n) {
+                sh.pair = j;
+                sh.base = base;
+                break;
+            }
+            base += n;
+        }
+    }
+    __syncthreads();
+    run.pair = sh.pair;
+    run.base = sh.base;
+    return run;
+}
+
+// The run's next piece; false at its end.
+template <int COLS, int T>
+__device__ __forceinline__ bool next_piece(const AttnArgs& a, Run& run, Piece& p) {
+    while (run.x < run.end && run.pair < a.v.n_seqs * a.row_tiles) {
+        int real = 0;
+        const int n = pair_tiles<COLS, T>(a, run.pair, &p.s, &p.rows, &real);
+        const int64_t all = (int64_t)n * a.v.kv_heads;
+        if (run.x >= run.base + all) {
+            run.base += all;
+            run.pair++;
+            continue;
+        }
+        const int64_t off = run.x - run.base;
+        p.b = run.pair / a.row_tiles;
+        p.f0 = run.pair % a.row_tiles * COLS;
+        p.head = (int)(off / n);
+        p.begin = (int)(off % n);
+        p.end = (int)min((int64_t)n, p.begin + (run.end - run.x));
+        run.x += p.end - p.begin;
+        p.pair = run.pair;
+        p.pieces = 0;
+        if (p.begin > 0) {
+            p.slot = 2 * (int)blockIdx.x;
+        } else if (p.end < n) {
+            p.slot = 2 * (int)blockIdx.x + 1;
+            p.pieces = 1 + (n - p.end + run.per - 1) / run.per;
+        } else {
+            p.slot = -1;
+        }
+        p.end = min(p.end, real);
+        return true;
+    }
+    return false;
 }
 
 // The kernel for chunks (paged_attention.cu).
 constexpr int kChunkRows = 256;  // (row, query head) pairs of a unit
 constexpr int kChunkKeys = 128;
-nvfp4_status launch_chunks(const AttnArgs& a, int64_t units, cudaStream_t stream);
+constexpr int kChunkCtas = 148;  // one an SM
+constexpr int kChunkLeast = 2;   // tiles of a run
+nvfp4_status launch_chunks(const AttnArgs& a, unsigned ctas, cudaStream_t stream);
 
 }  // namespace paged
 }  // namespace nvfp4

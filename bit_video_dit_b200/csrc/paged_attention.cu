@@ -1,9 +1,10 @@
 // Causal attention of chunks of new tokens over the paged NVFP4 cache on the
 // tensor cores (few rows a head: paged.cu).
 //
-// Work unit: one sequence, one K/V head, two tiles (A and B) of 128 (row, query
-// head of the group) pairs, so that a group's heads share the keys, and a run
-// of 128-key tiles.  Persistent CTAs, one an SM; inside a CTA
+// Work unit: one sequence, one K/V head and two tiles (A and B) of 128 (row,
+// query head of the group) pairs, so that a group's heads share the keys; the
+// units' 128-key tiles are dealt out in equal runs (paged.cuh), one a CTA and
+// SM.  Inside a CTA
 //   warps 0-3   softmax of tile A (thread = pair = TMEM lane),
 //   warps 4-7   softmax of tile B,
 //   warps 8-15  producers: a thread decodes half of one key's row of K and of V
@@ -12,7 +13,7 @@
 // The decoding is what the tensor cores wait for most: a unit pays 2 * 128 * d
 // elements of it for 4 * 256 * 128 * d operations, and one warp a scheduler
 // cannot issue it fast enough, hence eight producer warps.
-// Registers: 640 threads start with 96 each; the producers give 32 of theirs to
+// Registers: 640 threads start with 96 each; the producers give 24 of theirs to
 // the softmax (setmaxnreg).
 // Shared memory: Q_A, Q_B, K, V[2], P_A, P_B, each of 8 x 8 core matrices
 // without swizzle, element (row r, column c) at (c / 8) * 2048 + r * 16 +
@@ -41,7 +42,7 @@ constexpr int kTile = 128;  // pairs of a query tile, keys of a key tile
 constexpr int kProducer0 = 8, kMmaWarp = 16;  // first producer warp, the issuing warp
 constexpr int kThreads = 640;                 // five warpgroups
 constexpr int kProducers = 256, kSoft = 128;  // producer threads, threads of a softmax group
-constexpr int kLaunchRegs = 96, kSoftRegs = 128, kProducerRegs = 64;  // the last warpgroup keeps kLaunchRegs
+constexpr int kLaunchRegs = 96, kSoftRegs = 120, kProducerRegs = 72;  // the last warpgroup keeps kLaunchRegs
 static_assert(2 * kSoftRegs + 2 * kProducerRegs + kLaunchRegs <= 5 * kLaunchRegs, "registers of the block");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 0, kOCol = 256;
@@ -85,43 +86,6 @@ __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, Sha
     return false;
 }
 
-// A work unit; every role derives the same one from its number.
-struct Unit {
-    Seq s;
-    int b, head, f0, pairs, split, begin, end;
-    Span span;
-    int n_sink, first;  // of Tiles
-    bool valid, has_b;
-    __device__ __forceinline__ int key0(int i) const { return (i < n_sink ? i : first + i - n_sink) * kTile; }
-};
-
-__device__ __forceinline__ Unit get_unit(const AttnArgs& a, int u) {
-    Unit w;
-    w.split = u % a.splits;
-    u /= a.splits;
-    w.head = u % a.v.kv_heads;
-    u /= a.v.kv_heads;
-    // the rows of the last positions see the most keys: they come first
-    const int rt = a.row_tiles - 1 - u % a.row_tiles;
-    w.b = u / a.row_tiles;
-    w.s = load_seq(a.v, w.b);
-    w.valid = w.s.n <= a.max_rows;
-    if (!w.valid) record_error(a.v.err, NVFP4_ERR_DEVICE, (uint32_t)w.b);
-    w.f0 = rt * kChunkRows;
-    const Rows rows = unit_rows(a, w.s, w.f0, kChunkRows);
-    w.pairs = rows.n;
-    w.span = rows.span;
-    const Tiles<kTile> tiles(rows.span);
-    w.n_sink = tiles.n_sink;
-    w.first = tiles.first;
-    const int per = tiles_per_split(a, tiles.count);
-    w.begin = w.split * per;
-    w.end = min(tiles.count, w.begin + per);
-    if (rows.n == 0 || (w.split > 0 && w.begin >= w.end)) w.valid = false;
-    w.has_b = rows.n > kTile;
-    return w;
-}
-
 // ---- producers -------------------------------------------------------------
 // Half of one key's row of K or V as stored.
 template <int D>
@@ -136,11 +100,11 @@ struct HalfKV {
 };
 
 template <int D>
-__device__ __forceinline__ void fetch(const AttnArgs& a, const Unit& w, int i, int row, int half, HalfKV<D>& x) {
+__device__ __forceinline__ void fetch(const AttnArgs& a, const Piece& w, const Tiles<kTile>& tiles, int i, int row, int half, HalfKV<D>& x) {
     const View& v = a.v;
-    const int key = w.key0(i) + row;
+    const int key = tiles.key0(i) + row;
     int page = -1;
-    if (key < w.span.hi && group_seen(w.span, key & ~(kGroup - 1))) page = page_of(v, w.b, key);
+    if (key < w.rows.span.hi && group_seen(w.rows.span, key & ~(kGroup - 1))) page = page_of(v, w.b, key);
     if (page >= 0) {
         const int64_t r = cache_row(v, page, w.head, key);
 #pragma unroll
@@ -174,17 +138,18 @@ __device__ __forceinline__ void store_half(const HalfRow<D>& h, uint32_t base, i
 }
 
 template <int D>
-__device__ __forceinline__ void producer_role(const AttnArgs& a, Shared& sh, uint32_t smem0, int tid, int64_t units) {
+__device__ __forceinline__ void producer_role(const AttnArgs& a, Shared& sh, uint32_t smem0, int tid, Run run) {
     const int row = tid & (kTile - 1), half = tid / kTile;
     uint32_t ph_k = 0u, nv = 0u;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const Unit w = get_unit(a, (int)u);
-        if (!w.valid || w.begin >= w.end) continue;
+    Piece w;
+    while (next_piece<kChunkRows, kTile>(a, run, w)) {
+        if (w.begin >= w.end) continue;
+        const Tiles<kTile> tiles(w.rows.span);
         HalfKV<D> x;
-        fetch<D>(a, w, w.begin, row, half, x);
+        fetch<D>(a, w, tiles, w.begin, row, half, x);
         for (int i = w.begin; i < w.end; i++) {
             HalfKV<D> next;
-            if (i + 1 < w.end) fetch<D>(a, w, i + 1, row, half, next);
+            if (i + 1 < w.end) fetch<D>(a, w, tiles, i + 1, row, half, next);
             // a buffer's first fill passes at once (parity 1 of a fresh barrier)
             if (!wait_or_stop(&sh.k_empty, ph_k ^ 1u, sh, a, 4)) return;
             ph_k ^= 1u;
@@ -206,9 +171,9 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, Shared& sh, uin
 // Pair f of the unit's sequence into Q at row `row` (zeros past the last),
 // scaled by 2^k to binary16 (fp4mma.cuh); returns 2^-k.
 template <int D>
-__device__ __forceinline__ float load_q_row(const AttnArgs& a, const Unit& w, uint32_t q_s, int f, int row) {
+__device__ __forceinline__ float load_q_row(const AttnArgs& a, const Piece& w, uint32_t q_s, int f, int row) {
     uint4 v[D / 8];
-    if (f < w.f0 + w.pairs) {
+    if (f < w.f0 + w.rows.n) {
         const uint4* src = reinterpret_cast<const uint4*>(
             a.q + ((int64_t)(w.s.first + f / a.group) * a.ld_q + (int64_t)(w.head * a.group + f % a.group) * D) * 2);
 #pragma unroll
@@ -291,17 +256,18 @@ __device__ __forceinline__ float write_p(uint32_t t_s, uint32_t p_s, int row, co
 
 template <int D>
 __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint32_t smem0, uint32_t tmem, int X, int row,
-                                             int64_t units) {
+                                             Run run) {
     const uint32_t lane_off = (uint32_t)(row & ~31) << 16;
     const uint32_t t_s = tmem + kSCol + 128 * X + lane_off, t_o = tmem + kOCol + 128 * X + lane_off;
     const uint32_t q_s = smem0 + Smem<D>::q + X * Smem<D>::kOperand, p_s = smem0 + Smem<D>::p + X * Smem<D>::kP;
     const float ck = __ldg(a.v.a32[0]) * a.scale_log2, back = __ldg(a.v.a32[1]);
     uint32_t ph_s = 0u, ph_o = 0u;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const Unit w = get_unit(a, (int)u);
-        if (!w.valid || (X == 1 && !w.has_b)) continue;
+    Piece w;
+    while (next_piece<kChunkRows, kTile>(a, run, w)) {
+        if (X == 1 && w.rows.n <= kTile) continue;  // no tile B
+        const Tiles<kTile> tiles(w.rows.span);
         const int f = w.f0 + X * kTile + row;
-        const bool real = f < w.f0 + w.pairs;
+        const bool real = f < w.f0 + w.rows.n;
         float c_s = 0.0f;
         if (w.begin < w.end) {  // (without a key tile the issuing thread does not wait for it)
             c_s = load_q_row<D>(a, w, q_s, f, row) * ck;
@@ -313,7 +279,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
         float m = -INFINITY, l = 0.0f;
         bool first = true;
         for (int i = w.begin; i < w.end; i++) {
-            const int k0 = w.key0(i);
+            const int k0 = tiles.key0(i);
             const RowMask rm{lo - k0, hi - k0, a.sinks - k0};
             // (padding rows compute as if they saw everything)
             const bool all = __all_sync(0xFFFFFFFFu, !real || (rm.hi >= kTile && (rm.lo <= 0 || rm.sink >= kTile)));
@@ -363,9 +329,9 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
         }
         const int64_t orow = w.s.first + f / a.group;
         const int qh = w.head * a.group + f % a.group;
-        const int64_t slot = ((int64_t)w.split * a.v.n_rows + orow) * a.heads + qh;
+        const int64_t slot = (int64_t)w.slot * kChunkRows + f - w.f0;
         const float inv_l = l > 0.0f ? __fdiv_rn(back, l) : 0.0f;  // a row that sees no key: zeros
-        if (a.splits > 1 && real) a.part_ml[slot] = make_float2(m, l);
+        if (w.slot >= 0 && real) a.part_ml[slot] = make_float2(m, l);
 #pragma unroll
         for (int c = 0; c < D / 32; c++) {
             uint32_t r[32];
@@ -378,7 +344,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
                 for (int j = 0; j < 32; j++) r[j] = 0u;
             }
             if (!real) continue;
-            if (a.splits > 1) {
+            if (w.slot >= 0) {
                 float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + 32 * c);
 #pragma unroll
                 for (int g = 0; g < 8; g++)
@@ -415,7 +381,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
 //  - a unit's first products overwrite S_X, Q_X and O_X: q_full[X] of the unit
 //    is signalled after softmax X has read the last unit's O_X.
 template <int D>
-__device__ __forceinline__ void mma_role(const AttnArgs& a, Shared& sh, uint32_t smem0, uint32_t tmem, int64_t units) {
+__device__ __forceinline__ void mma_role(const AttnArgs& a, Shared& sh, uint32_t smem0, uint32_t tmem, Run run) {
     constexpr uint32_t ID_QK = idesc(0, kTile), ID_PV = idesc(1, D);
     auto qk = [&](int X) {
         const uint32_t q_s = smem0 + Smem<D>::q + X * Smem<D>::kOperand, k_s = smem0 + Smem<D>::k;
@@ -432,14 +398,17 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared& sh, uint32_t
             mma_f16(tmem + kOCol + 128 * X, smem_desc(p_s + k * 4096, 2048, 128, kLayoutNone),
                     smem_desc(v_s + k * 256, 128, 2048, kLayoutNone), ID_PV, (acc || k > 0) ? 1u : 0u);
     };
+    int4 cut = make_int4(0, 0, 0, 0);
     uint32_t ph_q[2] = {0u, 0u}, ph_p[2] = {0u, 0u}, ph_k = 0u, nv = 0u;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const Unit w = get_unit(a, (int)u);
-        if (!w.valid || w.begin >= w.end) continue;
+    Piece w;
+    while (ok && next_piece<kChunkRows, kTile>(a, run, w)) {
+        if (w.pieces) cut = make_int4(w.pieces, w.pair, w.head, 0);
+        if (w.begin >= w.end) continue;
+        const bool has_b = w.rows.n > kTile;
         if (!wait_or_stop(&sh.q_full[0], ph_q[0], sh, a, 6)) break;
         ph_q[0] ^= 1u;
-        if (w.has_b) {
+        if (has_b) {
             if (!wait_or_stop(&sh.q_full[1], ph_q[1], sh, a, 6)) break;
             ph_q[1] ^= 1u;
         }
@@ -447,7 +416,7 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared& sh, uint32_t
         ph_k ^= 1u;
         tc_fence_after();
         qk(0);
-        if (w.has_b) qk(1);
+        if (has_b) qk(1);
         tc_commit(&sh.k_empty);
         for (int i = w.begin; i < w.end; i++) {
             const bool more = i + 1 < w.end;
@@ -471,7 +440,7 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared& sh, uint32_t
             } else {
                 tc_commit(&sh.o_full[0]);
             }
-            if (w.has_b) {
+            if (has_b) {
                 if (!wait_or_stop(&sh.p_full[1], ph_p[1], sh, a, 9)) {
                     ok = false;
                     break;
@@ -483,13 +452,14 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared& sh, uint32_t
             tc_commit(&sh.v_empty[vb]);
             nv++;
             if (more) {
-                if (w.has_b) qk(1);
+                if (has_b) qk(1);
                 tc_commit(&sh.k_empty);
-            } else if (w.has_b) {
+            } else if (has_b) {
                 tc_commit(&sh.o_full[1]);
             }
         }
     }
+    a.cut[blockIdx.x] = cut;
     // every product issued is done before the TMEM is released (also after a stop)
     tc_commit(&sh.done);
     volatile int never = 0;
@@ -497,10 +467,12 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared& sh, uint32_t
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ AttnArgs a, int64_t units) {
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Shared sh;
+    __shared__ RunScratch scratch;
     const int warp = threadIdx.x >> 5;
+    const Run run = make_run<kChunkRows, kTile, kThreads>(a, kChunkLeast, scratch);
     if (threadIdx.x == 0) {
         for (int X = 0; X < 2; X++) {
             mbar_init(&sh.q_full[X], kSoft);
@@ -526,12 +498,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const uint32_t tmem = sh.tmem_base, smem0 = smem_u32(smem);
     if (warp < kProducer0) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        softmax_role<D>(a, sh, smem0, tmem, warp >> 2, threadIdx.x & (kSoft - 1), units);
+        softmax_role<D>(a, sh, smem0, tmem, warp >> 2, threadIdx.x & (kSoft - 1), run);
     } else if (warp < kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-        producer_role<D>(a, sh, smem0, threadIdx.x - kProducer0 * 32, units);
+        producer_role<D>(a, sh, smem0, threadIdx.x - kProducer0 * 32, run);
     } else if (threadIdx.x == kMmaWarp * 32) {
-        mma_role<D>(a, sh, smem0, tmem, units);
+        mma_role<D>(a, sh, smem0, tmem, run);
     }
     tc_fence_before();
     __syncthreads();
@@ -543,13 +515,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 }
 
 template <int D>
-nvfp4_status launch(const AttnArgs& a, int64_t units, cudaStream_t stream) {
+nvfp4_status launch(const AttnArgs& a, unsigned ctas, cudaStream_t stream) {
     static PerDevice<int> ready;
-    int sms = 0;
-    const nvfp4_status st = ready.get(&sms, [](int dev, int& n) {
+    int done = 0;
+    const nvfp4_status st = ready.get(&done, [](int, int& v) {
         cudaFuncAttributes at;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1 ||
-            cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes) !=
+        v = 1;
+        if (cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes) !=
                 cudaSuccess ||
             cudaFuncGetAttributes(&at, chunk_kernel<D>) != cudaSuccess)
             return NVFP4_ERR_CUDA;
@@ -557,15 +529,14 @@ nvfp4_status launch(const AttnArgs& a, int64_t units, cudaStream_t stream) {
         return at.numRegs == kLaunchRegs ? NVFP4_OK : NVFP4_ERR_UNSUPPORTED;
     });
     if (st != NVFP4_OK) return st;
-    const unsigned grid = (unsigned)std::min<int64_t>(units, sms);
-    chunk_kernel<D><<<grid, kThreads, Smem<D>::bytes, stream>>>(a, units);
+    chunk_kernel<D><<<ctas, kThreads, Smem<D>::bytes, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
 }  // namespace
 
-nvfp4_status launch_chunks(const AttnArgs& a, int64_t units, cudaStream_t stream) {
-    return a.v.d == 128 ? launch<128>(a, units, stream) : launch<64>(a, units, stream);
+nvfp4_status launch_chunks(const AttnArgs& a, unsigned ctas, cudaStream_t stream) {
+    return a.v.d == 128 ? launch<128>(a, ctas, stream) : launch<64>(a, ctas, stream);
 }
 
 }  // namespace paged

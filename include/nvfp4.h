@@ -422,9 +422,9 @@ typedef struct {
  * device memory and are read by the kernels, so a captured call follows their
  * contents.  Rows behind row_start[n_seqs] belong to no sequence and are left
  * as they were.  n_b = 0 is a sequence that takes no part.
- * max_rows and max_len bound n_b and lens[b] on the host's side: max_rows sizes
- * the launch; max_len only guides how it is split (a longer sequence is still
- * read whole).
+ * max_rows and max_len bound n_b and lens[b] on the host's side: max_rows says
+ * which rows a launch covers; max_len only how many CTAs share the keys (a
+ * longer sequence is still read whole).
  * Reported as NVFP4_ERR_DEVICE (info = the sequence): a row range that is not
  * ascending within [0, n_rows], a negative length, and for the attention more
  * than max_rows rows (the sequence is skipped); a page entry that is needed and
@@ -469,12 +469,13 @@ nvfp4_status nvfp4_paged_gather(const nvfp4_paged_cache* cache, const nvfp4_page
  * binary16.  A row that sees no key gives zeros.  Pages that hold no visible
  * key are not looked up, so a window's caller may have given them back.
  * workspace: nvfp4_paged_attention_workspace_bytes of the same arguments (0:
- * refused), which grows with n_rows; results do not depend on what it holds
- * behind the control block.  Up to 16 (row, query head) pairs a K/V head
+ * refused; at most 40 MB); results do not depend on what it
+ * holds behind the control block.  Up to 16 (row, query head) pairs a K/V head
  * (max_rows * heads / kv_heads) run on a kernel for decode steps, more on one
  * for chunks (tcgen05), whose waits are bounded: one that runs out records
- * NVFP4_ERR_TIMEOUT (info = which wait) and leaves o incomplete.  One launch, or
- * two when long sequences are split over CTAs. */
+ * NVFP4_ERR_TIMEOUT (info = which wait) and leaves o incomplete.  Both deal the
+ * key tiles out to the CTAs in equal runs, whatever the lengths; a second launch
+ * joins the rows whose keys lie in several runs. */
 size_t nvfp4_paged_attention_workspace_bytes(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows,
                                              int32_t heads, int32_t window, int32_t sinks);
 nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows, const void* q_bf16,
