@@ -150,8 +150,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
 // attention of few rows.
 //
 // Unit: one sequence, one K/V head, up to 8 NT rows (row, query head of the
-// group) and a run of 32-key tiles; 4 warps take the tiles in turn, each with
-// its own running maximum and sum.  Both products have the cache as the A
+// group); the units' 32-key tiles are dealt out in equal runs, one a warp
+// (paged.cuh): warps that wait for nobody hide one another's beginnings and
+// ends of units.  Both products have the cache as the A
 // operand (S^T = K Q^T, O^T = V^T P^T), so eight rows fill a matrix
 // instruction's columns; a lane reads whole 16-byte (K) and 8-byte (V) pieces of
 // rows, with the contraction's columns permuted to fit, and P^T comes from S^T
@@ -159,8 +160,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
 // tiles in shared memory a warp, so that no registers wait for them.
 //
 // Bound: the cache's bytes (a key and value are 9/8 head_dim bytes a head),
-// and beside them the decoding (fp4mma.cuh).  Long sequences are split over
-// CTAs and joined by combine_kernel.
+// and beside them the decoding (fp4mma.cuh).
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 32;  // keys of a tile
 constexpr int kSms = 148;
@@ -197,15 +197,37 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int n) 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
+// A lane's share of a tile's copies: where it reads (add row * (D / 2) or row *
+// (D / 16)) and the key that its first chunk belongs to.
+template <int D>
+struct CopyLane {
+    static constexpr int kChunks = D / 32;                // of a row of codes
+    static constexpr int kRows = 32 / kChunks;            // rows that the warp copies at a time
+    static constexpr int kScaleChunks = kKeys * D / 256;  // of a tensor
+    const uint8_t *k, *v, *s;
+    uint32_t dk, dv, ds;  // the same in a ring slot
+    int key, skey;
+    bool scales;
+    __device__ __forceinline__ CopyLane(const View& a, int lane) {
+        const int c = lane % kChunks, t = lane / kScaleChunks, i = lane % kScaleChunks;
+        key = lane / kChunks;
+        k = a.codes[0] + key * (D / 2) + 16 * c;
+        v = a.codes[1] + key * (D / 2) + 16 * c;
+        dk = Ring<D>::k + key * (D / 2) + 16 * c;
+        dv = Ring<D>::v + key * (D / 2) + 16 * (D == 128 ? c ^ (key & 2) : c);  // (key & 2 is the same 8 or 16 rows on)
+        scales = t < 2;
+        skey = i * (256 / D);
+        s = a.scales[t & 1] + (skey & (kGroup - 1)) * (D / 16);
+        ds = (t ? Ring<D>::vs : Ring<D>::ks) + 16 * i;
+    }
+};
+
 // Tile at key k0 into a ring slot.  Groups that no row sees, and what lies
 // behind the last key (it is not a value), become zeros.
 template <int D>
-__device__ __forceinline__ void load_tile(const View& v, int b, uint32_t head_row, const Span& sp, int k0, int lane,
-                                          const int* pages, uint32_t dst) {
-    constexpr int kChunks = D / 32;            // of a row of codes
-    constexpr int kRows = 32 / kChunks;        // rows that the warp copies at a time
-    constexpr int kScaleChunks = kKeys * D / 256;
-    const uint32_t page_rows = (uint32_t)v.kv_heads * (uint32_t)v.page_size;
+__device__ __forceinline__ void load_tile(const View& v, const CopyLane<D>& ln, int b, uint32_t page_rows,
+                                          uint32_t head_row, const Span& sp, int k0, const int* pages, uint32_t dst) {
+    constexpr int kRows = CopyLane<D>::kRows;
     uint32_t row[2];
     bool ok[2];
 #pragma unroll
@@ -216,22 +238,32 @@ __device__ __forceinline__ void load_tile(const View& v, int b, uint32_t head_ro
         const int at = v.page_shift >= 0 ? kq & (v.page_size - 1) : kq % v.page_size;
         row[q] = ok[q] ? (uint32_t)pages[q] * page_rows + head_row + (uint32_t)at : 0u;  // below 2^32 (host)
     }
-    const int r0 = lane / kChunks, c = lane % kChunks;
+    if (ok[0] && ok[1] && k0 + kKeys <= sp.hi) {
 #pragma unroll
-    for (int j = 0; j < kKeys / kRows; j++) {
-        const int key = j * kRows + r0, q = j * kRows / 16;
-        const uint64_t off = (uint64_t)(row[q] + (uint32_t)(key - 16 * q)) * (D / 2) + 16 * c;
-        const int n = ok[q] && k0 + key < sp.hi ? 16 : 0;
-        const int cv = D == 128 ? c ^ (key & 2) : c;
-        copy16(dst + Ring<D>::k + key * (D / 2) + 16 * c, v.codes[0] + off, n);
-        copy16(dst + Ring<D>::v + key * (D / 2) + 16 * cv, v.codes[1] + off, n);
-    }
-    if (lane < 2 * kScaleChunks) {
-        const int t = lane / kScaleChunks, i = lane % kScaleChunks;  // K or V, its chunk
-        const int key = i * (256 / D);
-        const uint64_t off = (uint64_t)((key < 16 ? row[0] : row[1] - 16u) + (uint32_t)key) * (D / 16);
-        const int n = (key < 16 ? ok[0] : ok[1]) ? min(16, max(0, sp.hi - k0 - key) * (D / 16)) : 0;
-        copy16(dst + (t ? Ring<D>::vs : Ring<D>::ks) + 16 * i, v.scales[t] + off, n);
+        for (int q = 0; q < 2; q++) {
+            const uint8_t *k = ln.k + (uint64_t)row[q] * (D / 2), *w = ln.v + (uint64_t)row[q] * (D / 2);
+#pragma unroll
+            for (int j = 0; j < 16 / kRows; j++) {
+                copy16(dst + ln.dk + (16 * q + j * kRows) * (D / 2), k + j * kRows * (D / 2), 16);
+                copy16(dst + ln.dv + (16 * q + j * kRows) * (D / 2), w + j * kRows * (D / 2), 16);
+            }
+        }
+        if (ln.scales) copy16(dst + ln.ds, ln.s + (uint64_t)(ln.skey < 16 ? row[0] : row[1]) * (D / 16), 16);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            const uint8_t *k = ln.k + (uint64_t)row[q] * (D / 2), *w = ln.v + (uint64_t)row[q] * (D / 2);
+#pragma unroll
+            for (int j = 0; j < 16 / kRows; j++) {
+                const int n = ok[q] && k0 + 16 * q + j * kRows + ln.key < sp.hi ? 16 : 0;
+                copy16(dst + ln.dk + (16 * q + j * kRows) * (D / 2), k + j * kRows * (D / 2), n);
+                copy16(dst + ln.dv + (16 * q + j * kRows) * (D / 2), w + j * kRows * (D / 2), n);
+            }
+        }
+        if (ln.scales) {
+            const int n = (ln.skey < 16 ? ok[0] : ok[1]) ? min(16, max(0, sp.hi - k0 - ln.skey) * (D / 16)) : 0;
+            copy16(dst + ln.ds, ln.s + (uint64_t)(ln.skey < 16 ? row[0] : row[1]) * (D / 16), n);
+        }
     }
 }
 
@@ -271,8 +303,6 @@ __device__ __forceinline__ void decode_k(const uint32_t* c, uint32_t sc, uint32_
 
 template <int D>
 constexpr int decode_smem() {
-    // (the join's buffers, 16 columns at most, are smaller)
-    static_assert(kWarps * 16 * ((D + 4) * 4 + 8) <= kWarps * Ring<D>::kStages * Ring<D>::bytes, "join");
     return kWarps * Ring<D>::kStages * Ring<D>::bytes;
 }
 
@@ -283,38 +313,43 @@ constexpr int decode_ctas() {
 }
 
 template <int D, int NT>
-__device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, uint8_t* ring_mem) {
+__device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, uint32_t ring) {
     constexpr int kCols = 8 * NT, kSteps = D / 16, kPer = D / 8;  // kPer: a lane's channels of O
     const View& v = a.v;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const Seq& s = u.s;
     const Rows& rows = u.rows;
     const int b = u.b, head = u.head, f0 = u.f0, begin = u.begin, end = u.end;
     const Tiles<kKeys> tiles(rows.span);
 
-    const uint32_t ring = smem_u32(ring_mem) + (uint32_t)(warp * Ring<D>::kStages * Ring<D>::bytes);
+    const uint32_t page_rows = (uint32_t)v.kv_heads * (uint32_t)v.page_size;
     const uint32_t head_row = (uint32_t)head * (uint32_t)v.page_size;
+    const CopyLane<D> ln(v, lane);
     const int32_t* table = v.pages + (int64_t)b * v.max_pages;
 
-    // the warp's tiles begin + warp, + kWarps, ..: copies run kStages - 1 tiles ahead, page lookups one more
+    // copies run kStages - 1 tiles ahead, page lookups one more
     int pages[2];
     auto lookup = [&](int i) {
         if (i < end) {
             const int k0 = tiles.key0(i);
             pages[0] = group_page(v, table, rows.span, k0);
-            pages[1] = group_page(v, table, rows.span, k0 + 16);
+            // (a page of 2^5 or more tokens holds both groups of a tile)
+            pages[1] = v.page_shift >= 5 && pages[0] >= 0 && group_seen(rows.span, k0 + 16)
+                           ? pages[0]
+                           : group_page(v, table, rows.span, k0 + 16);
         }
     };
     auto fetch = [&](int i, int slot) {
         if (i < end)
-            load_tile<D>(v, b, head_row, rows.span, tiles.key0(i), lane, pages, ring + (uint32_t)(slot * Ring<D>::bytes));
+            load_tile<D>(v, ln, b, page_rows, head_row, rows.span, tiles.key0(i), pages,
+                         ring + (uint32_t)(slot * Ring<D>::bytes));
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    lookup(begin + warp);
+    lookup(begin);
 #pragma unroll
     for (int i = 0; i < Ring<D>::kStages - 1; i++) {
-        fetch(begin + warp + i * kWarps, i);
-        lookup(begin + warp + (i + 1) * kWarps);
+        fetch(begin + i, i);
+        lookup(begin + i + 1);
     }
 
     // queries: column n of tile j is row f0 + 8 j + n; columns past the last row are zeros and nobody reads them
@@ -362,12 +397,12 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
     int slot = 0;
 
 #pragma unroll 1
-    for (int i = begin + warp; i < end; i += kWarps) {
+    for (int i = begin; i < end; i++) {
         const int k0 = tiles.key0(i);
         asm volatile("cp.async.wait_group %0;" ::"n"(Ring<D>::kStages - 2) : "memory");
         __syncwarp();  // the tile is there for every lane, and every lane has left the slot that is filled next
-        fetch(i + (Ring<D>::kStages - 1) * kWarps, (slot + Ring<D>::kStages - 1) % Ring<D>::kStages);
-        lookup(i + Ring<D>::kStages * kWarps);
+        fetch(i + Ring<D>::kStages - 1, (slot + Ring<D>::kStages - 1) % Ring<D>::kStages);
+        lookup(i + Ring<D>::kStages);
         const uint32_t at = ring + (uint32_t)(slot * Ring<D>::bytes);
         slot = (slot + 1) % Ring<D>::kStages;
         // z: the scores' exponents, relative to the reference: 2^z is the weight
@@ -484,12 +519,9 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
                     mma_16816(o[j][r], va[2 * r], va[2 * r + 1], vb[2 * r], vb[2 * r + 1], pb[j][0], pb[j][1]);
         }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();  // the ring's memory is the join's from here on
+    __syncwarp();  // every lane has left the ring (its copies are done: none was begun behind the last tile)
 
-    // join the four warps
-    float(*so)[kCols][D + 4] = reinterpret_cast<float(*)[kCols][D + 4]>(ring_mem);
-    float2(*sml)[kCols] = reinterpret_cast<float2(*)[kCols]>(ring_mem + kWarps * kCols * (D + 4) * 4);
+    const float back = __ldg(v.a32[1]);
 #pragma unroll
     for (int j = 0; j < NT; j++)
 #pragma unroll
@@ -497,58 +529,51 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
             float sum = l[j][e];
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-            if (g == 0) sml[warp][8 * j + 2 * t + e] = make_float2(limit[j][e] == kLazy ? -nm[j][e] : kFloor, sum);
+            const int n = 8 * j + 2 * t + e;  // the lane holds channels kPer g .. of this row
+            if (n >= rows.n) continue;
+            if (u.slot >= 0) {
+                const int64_t at = (int64_t)u.slot * kCols + n;
+                float4* dst = reinterpret_cast<float4*>(a.part_o + at * D + kPer * g);
 #pragma unroll
-            for (int r = 0; r < kSteps; r++) {
-                so[warp][8 * j + 2 * t + e][kPer * g + 2 * r] = o[j][r][e];
-                so[warp][8 * j + 2 * t + e][kPer * g + 2 * r + 1] = o[j][r][e + 2];
+                for (int r = 0; r < kSteps; r += 2)
+                    dst[r / 2] = make_float4(o[j][r][e], o[j][r][e + 2], o[j][r + 1][e], o[j][r + 1][e + 2]);
+                if (g == 0) a.part_ml[at] = make_float2(limit[j][e] == kLazy ? -nm[j][e] : kFloor, sum);
+            } else {
+                const float f = sum > 0.0f ? __fdiv_rn(back, sum) : 0.0f;  // a row that sees no key: zeros
+                const int row = s.first + (f0 + n) / a.group, qh = head * a.group + (f0 + n) % a.group;
+                uint4* dst = reinterpret_cast<uint4*>(a.o + ((int64_t)row * a.ld_o + (int64_t)qh * D + kPer * g) * 2);
+#pragma unroll
+                for (int r = 0; r < kSteps; r += 4) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(o[j][r + i][e] * f, o[j][r + i][e + 2] * f);
+                        y[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    dst[r / 4] = make_uint4(y[0], y[1], y[2], y[3]);
+                }
             }
         }
-    __syncthreads();
-    const float back = __ldg(v.a32[1]);
-    for (int i = threadIdx.x; i < rows.n * (D / 2); i += kWarps * 32) {
-        const int n = i / (D / 2), d = i % (D / 2) * 2;
-        float mx = sml[0][n].x;
-#pragma unroll
-        for (int w = 1; w < kWarps; w++) mx = fmaxf(mx, sml[w][n].x);
-        float sum = 0.0f, y0 = 0.0f, y1 = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            const float f = ex2(sml[w][n].x - mx);
-            sum += sml[w][n].y * f;
-            y0 += so[w][n][d] * f;
-            y1 += so[w][n][d + 1] * f;
-        }
-        if (u.slot >= 0) {
-            const int64_t at = (int64_t)u.slot * kCols + n;
-            *reinterpret_cast<float2*>(a.part_o + at * D + d) = make_float2(y0, y1);
-            if (d == 0) a.part_ml[at] = make_float2(mx, sum);
-        } else {
-            const int row = s.first + (f0 + n) / a.group, qh = head * a.group + (f0 + n) % a.group;
-            const float f = sum > 0.0f ? __fdiv_rn(back, sum) : 0.0f;  // a row that sees no key: zeros
-            *reinterpret_cast<__nv_bfloat162*>(a.o + ((int64_t)row * a.ld_o + (int64_t)qh * D + d) * 2) =
-                __floats2bfloat162_rn(y0 * f, y1 * f);
-        }
-    }
-    __syncthreads();  // the next piece fills the ring again
 }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(128) uint8_t ring_mem[];
-    __shared__ RunScratch scratch;
-    // no run shorter than a tile a warp
-    Run run = make_run<8 * NT, kKeys, kWarps * 32>(a, kWarps, scratch);
+    RunScratch<kWarps * 32>& scratch = *reinterpret_cast<RunScratch<kWarps * 32>*>(ring_mem);
+    const int warp = threadIdx.x >> 5;
+    const uint32_t ring = smem_u32(ring_mem) + (uint32_t)(warp * Ring<D>::kStages * Ring<D>::bytes);
+    Run run = make_run<8 * NT, kKeys, kWarps * 32, kWarps>(a, warp, 1, scratch);
+    __syncthreads();  // the rings take the scratch memory over
     Piece u;
     int4 cut = make_int4(0, 0, 0, 0);
     while (next_piece<8 * NT, kKeys>(a, run, u)) {
-        decode_piece<D, NT>(a, u, ring_mem);
+        decode_piece<D, NT>(a, u, ring);
         if (u.pieces) cut = make_int4(u.pieces, u.pair, u.head, 0);
     }
-    if (threadIdx.x == 0) a.cut[blockIdx.x] = cut;
+    if ((threadIdx.x & 31) == 0) a.cut[run.worker] = cut;
 }
 
-// Joins the pieces of the unit that CTA blockIdx.x began, a warp a row.
+// Joins the pieces of the unit that worker blockIdx.x began, a warp a row.
 template <int D, int COLS>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnArgs a) {
     const View& v = a.v;
@@ -558,7 +583,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     const Seq s = load_seq(v, cut.y / a.row_tiles);
     const int f = cut.y % a.row_tiles * COLS + n;
     if (n >= COLS || f >= s.n * a.group) return;
-    // piece 0 is the end of this CTA's run, piece p the beginning of CTA p later
+    // piece 0 is the end of this worker's run, piece p the beginning of the p-th later one's
     auto at = [&](int p) { return (int64_t)(2 * ((int)blockIdx.x + p) + (p == 0)) * COLS + n; };
     float mx = kFloor, sum = 0.0f, y[D / 32];
 #pragma unroll
@@ -680,7 +705,7 @@ nvfp4_status rows_call(bool append, const nvfp4_paged_cache* c, const nvfp4_page
 struct Plan {
     bool chunks;  // chunk_kernel (paged_attention.cu), else decode_kernel
     int cols;     // (row, query head) pairs of a unit
-    int row_tiles, ctas;
+    int row_tiles, ctas, workers;
     size_t cut, ml, o, ws;  // bytes from the workspace's start
 };
 
@@ -697,12 +722,14 @@ bool make_plan(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, int heads,
     int64_t seen = r->max_len;
     if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + sinks + std::min<int64_t>(r->max_rows, p->cols));
     const int keys = p->chunks ? kChunkKeys : kKeys, least = p->chunks ? kChunkLeast : kWarps;
+    p->workers = p->chunks ? 1 : kWarps;  // of a CTA
     const int64_t tiles = (seen / keys + 3) * p->row_tiles * std::max(1, r->n_seqs);  // ragged at both ends and the sinks'
     p->ctas = (int)std::min<int64_t>(p->ctas, (tiles * c->kv_heads + least - 1) / least);
     p->cut = kControl;
-    p->ml = p->cut + (size_t)p->ctas * sizeof(int4);
-    p->o = p->ml + (size_t)p->ctas * 2 * p->cols * sizeof(float2);
-    p->ws = p->o + (size_t)p->ctas * 2 * p->cols * c->head_dim * sizeof(float);
+    p->workers *= p->ctas;
+    p->ml = p->cut + (size_t)p->workers * sizeof(int4);
+    p->o = p->ml + (size_t)p->workers * 2 * p->cols * sizeof(float2);
+    p->ws = p->o + (size_t)p->workers * 2 * p->cols * c->head_dim * sizeof(float);
     return true;
 }
 
@@ -800,6 +827,6 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, co
         cache->head_dim == 128
             ? (p.chunks ? combine_kernel<128, kChunkRows> : p.cols == 8 ? combine_kernel<128, 8> : combine_kernel<128, 16>)
             : (p.chunks ? combine_kernel<64, kChunkRows> : p.cols == 8 ? combine_kernel<64, 8> : combine_kernel<64, 16>);
-    join<<<dim3((unsigned)p.ctas, (unsigned)(p.cols / 8)), 256, 0, (cudaStream_t)stream>>>(a);
+    join<<<dim3((unsigned)p.workers, (unsigned)(p.cols / 8)), 256, 0, (cudaStream_t)stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }

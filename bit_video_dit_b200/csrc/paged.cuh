@@ -100,6 +100,14 @@ __device__ __forceinline__ bool group_seen(const Span& s, int k0) {
 // ---------------------------------------------------------------------------
 // attention: what the kernel for few rows and the one for chunks share
 // ---------------------------------------------------------------------------
+// The kernel for chunks (paged_attention.cu).
+constexpr int kChunkRows = 256;  // (row, query head) pairs of a unit
+constexpr int kChunkKeys = 128;
+constexpr int kChunkCtas = 148;  // one an SM
+constexpr int kChunkLeast = 2;   // tiles of a run
+struct AttnArgs;
+nvfp4_status launch_chunks(const AttnArgs& a, unsigned ctas, cudaStream_t stream);
+
 constexpr float kLazy = 8.0f;     // a reference maximum moves when exceeded by more than 2^8
 constexpr float kFloor = -1e30f;  // the reference before any visible key
 
@@ -111,9 +119,9 @@ struct AttnArgs {
     int heads, group, window, sinks, max_rows;
     int row_tiles;  // units of the most rows a sequence may have
     float scale_log2;
-    int4* cut;        // [CTAs]: (pieces of the unit that the CTA begins and does not end, or 0; its pair, head)
-    float* part_o;    // [CTAs][2][cols][d] unnormalised
-    float2* part_ml;  // [CTAs][2][cols] (reference maximum, sum)
+    int4* cut;        // [workers]: (pieces of the unit that it begins and does not end, or 0; its pair, head)
+    float* part_o;    // [workers][2][cols][d] unnormalised
+    float2* part_ml;  // [workers][2][cols] (reference maximum, sum)
 };
 
 // Rows f0 .. f0 + cols - 1 of a sequence's n * group (row, query head) pairs.
@@ -137,10 +145,10 @@ __device__ __forceinline__ Rows unit_rows(const AttnArgs& a, const Seq& s, int f
 
 // The work of a launch is one list of key tiles: for every pair of a sequence
 // and a run of its rows, for every K/V head, that unit's tiles.  The list is
-// cut into equal runs, one a CTA, whatever the lengths; a unit that lies in
-// several runs leaves a piece in each, which combine_kernel joins.  CTA k keeps
-// the piece of a unit that began before its run at 2 k, of one that ends after
-// it at 2 k + 1.
+// cut into equal runs, one a worker (a warp of the decode kernel, a CTA of the
+// chunk kernel), whatever the lengths; a unit that lies in several runs leaves
+// a piece in each, which combine_kernel joins.  Worker k keeps the piece of a
+// unit that began before its run at 2 k, of one that ends after it at 2 k + 1.
 struct Piece {
     int b, head, f0;   // sequence, K/V head, first (row, query head) pair
     int begin, end;    // tiles of the unit (a unit that sees none has one empty piece: 0, 0)
@@ -152,10 +160,15 @@ struct Piece {
 
 struct Run {
     int64_t x, end, base;  // the run's next tile and end, first tile of the pair
-    int pair, per;
+    int worker, pair, per;
 };
 
-// Tiles of pair j (0: no rows; a unit that sees no key counts as one tile).
+// What beginning and ending a unit costs, in tiles: a unit counts as that many
+// more, so that runs of short units are no longer than the others.
+template <int COLS>
+constexpr int kUnitCost = COLS == kChunkRows ? 1 : 5;
+
+// Tiles of pair j as counted in the list (0: no rows), and as they are.
 template <int COLS, int T>
 __device__ __forceinline__ int pair_tiles(const AttnArgs& a, int j, Seq* seq, Rows* rows, int* real) {
     const int b = j / a.row_tiles;
@@ -168,18 +181,19 @@ __device__ __forceinline__ int pair_tiles(const AttnArgs& a, int j, Seq* seq, Ro
     if (rows->n == 0) return 0;
     const Tiles<T> tiles(rows->span);
     *real = tiles.count;
-    return max(1, tiles.count);
+    return tiles.count + kUnitCost<COLS>;
 }
 
+template <int THREADS>
 struct RunScratch {
-    long long warp_sum[32];
-    long long base;
-    int pair;
+    long long warp_sum[THREADS / 32];
+    long long first[THREADS];  // first tile of each thread's pairs
 };
 
-// The CTA's run (all THREADS threads; none is shorter than `least` tiles).
-template <int COLS, int T, int THREADS>
-__device__ __forceinline__ Run make_run(const AttnArgs& a, int least, RunScratch& sh) {
+// The run of worker blockIdx.x * WORKERS + worker (all THREADS threads; no run
+// is shorter than `least` tiles).
+template <int COLS, int T, int THREADS, int WORKERS>
+__device__ __forceinline__ Run make_run(const AttnArgs& a, int worker, int least, RunScratch<THREADS>& sh) {
     const int pairs = a.v.n_seqs * a.row_tiles, each = (pairs + THREADS - 1) / THREADS;
     const int j0 = min(pairs, (int)threadIdx.x * each), j1 = min(pairs, j0 + each);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -188,6 +202,7 @@ __device__ __forceinline__ Run make_run(const AttnArgs& a, int least, RunScratch
     int real;
     long long sum = 0;
     for (int j = j0; j < j1; j++) sum += pair_tiles<COLS, T>(a, j, &s, &r, &real);
+    sum *= a.v.kv_heads;
     long long incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -195,7 +210,6 @@ __device__ __forceinline__ Run make_run(const AttnArgs& a, int least, RunScratch
         if (lane >= d) incl += y;
     }
     if (lane == 31) sh.warp_sum[warp] = incl;
-    if (threadIdx.x == 0) sh.pair = pairs;
     __syncthreads();
     long long before = 0, total = 0;
 #pragma unroll
@@ -203,27 +217,27 @@ __device__ __forceinline__ Run make_run(const AttnArgs& a, int least, RunScratch
         if (w < warp) before += sh.warp_sum[w];
         total += sh.warp_sum[w];
     }
-    total *= a.v.kv_heads;
-    Run run;
-    run.per = (int)max((long long)least, (total + gridDim.x - 1) / gridDim.x);
-    run.x = (int64_t)blockIdx.x * run.per;
-    run.end = min((int64_t)total, run.x + run.per);
-    long long base = (before + incl - sum) * a.v.kv_heads;
-    if (base <= run.x && run.x < base + sum * a.v.kv_heads) {
-        for (int j = j0; j < j1; j++) {
-            const long long n = (long long)pair_tiles<COLS, T>(a, j, &s, &r, &real) * a.v.kv_heads;
-            if (run.x < base + n) {
-                sh.pair = j;
-                sh.base = base;
-                break;
-            }
-            base += n;
-        }
-    }
+    sh.first[threadIdx.x] = before + incl - sum;
     __syncthreads();
-    run.pair = sh.pair;
-    run.base = sh.base;
-    return run;
+    const long long workers = (long long)gridDim.x * WORKERS;
+    Run run;
+    run.worker = (int)blockIdx.x * WORKERS + worker;
+    run.per = (int)max((long long)least, (total + workers - 1) / workers);
+    run.x = (int64_t)run.worker * run.per;
+    run.end = min((int64_t)total, run.x + run.per);
+    run.pair = pairs;
+    run.base = 0;
+    if (run.x >= run.end) return run;
+    // the last thread whose pairs begin at or before the run, then the pair among them
+    int lo = 0, hi = THREADS;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (sh.first[mid] <= run.x) lo = mid;
+        else hi = mid;
+    }
+    run.pair = lo * each;
+    run.base = sh.first[lo];
+    return run;  // (next_piece walks on from there)
 }
 
 // The run's next piece; false at its end.
@@ -245,28 +259,22 @@ __device__ __forceinline__ bool next_piece(const AttnArgs& a, Run& run, Piece& p
         p.begin = (int)(off % n);
         p.end = (int)min((int64_t)n, p.begin + (run.end - run.x));
         run.x += p.end - p.begin;
+        if (p.begin >= real && p.begin > 0) continue;  // the unit's cost alone is left
+        p.end = min(p.end, real);
         p.pair = run.pair;
         p.pieces = 0;
         if (p.begin > 0) {
-            p.slot = 2 * (int)blockIdx.x;
-        } else if (p.end < n) {
-            p.slot = 2 * (int)blockIdx.x + 1;
-            p.pieces = 1 + (n - p.end + run.per - 1) / run.per;
+            p.slot = 2 * run.worker;
+        } else if (p.end < real) {
+            p.slot = 2 * run.worker + 1;
+            p.pieces = 1 + (real - p.end + run.per - 1) / run.per;
         } else {
             p.slot = -1;
         }
-        p.end = min(p.end, real);
         return true;
     }
     return false;
 }
-
-// The kernel for chunks (paged_attention.cu).
-constexpr int kChunkRows = 256;  // (row, query head) pairs of a unit
-constexpr int kChunkKeys = 128;
-constexpr int kChunkCtas = 148;  // one an SM
-constexpr int kChunkLeast = 2;   // tiles of a run
-nvfp4_status launch_chunks(const AttnArgs& a, unsigned ctas, cudaStream_t stream);
 
 }  // namespace paged
 }  // namespace nvfp4

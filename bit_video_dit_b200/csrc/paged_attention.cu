@@ -13,7 +13,7 @@
 // The decoding is what the tensor cores wait for most: a unit pays 2 * 128 * d
 // elements of it for 4 * 256 * 128 * d operations, and one warp a scheduler
 // cannot issue it fast enough, hence eight producer warps.
-// Registers: 640 threads start with 96 each; the producers give 24 of theirs to
+// Registers: 640 threads start with 96 each; the producers give 16 of theirs to
 // the softmax (setmaxnreg).
 // Shared memory: Q_A, Q_B, K, V[2], P_A, P_B, each of 8 x 8 core matrices
 // without swizzle, element (row r, column c) at (c / 8) * 2048 + r * 16 +
@@ -42,7 +42,7 @@ constexpr int kTile = 128;  // pairs of a query tile, keys of a key tile
 constexpr int kProducer0 = 8, kMmaWarp = 16;  // first producer warp, the issuing warp
 constexpr int kThreads = 640;                 // five warpgroups
 constexpr int kProducers = 256, kSoft = 128;  // producer threads, threads of a softmax group
-constexpr int kLaunchRegs = 96, kSoftRegs = 120, kProducerRegs = 72;  // the last warpgroup keeps kLaunchRegs
+constexpr int kLaunchRegs = 96, kSoftRegs = 112, kProducerRegs = 80;  // the last warpgroup keeps kLaunchRegs
 static_assert(2 * kSoftRegs + 2 * kProducerRegs + kLaunchRegs <= 5 * kLaunchRegs, "registers of the block");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 0, kOCol = 256;
@@ -470,9 +470,9 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Shared sh;
-    __shared__ RunScratch scratch;
+    RunScratch<kThreads>& scratch = *reinterpret_cast<RunScratch<kThreads>*>(smem);  // before the operands are there
     const int warp = threadIdx.x >> 5;
-    const Run run = make_run<kChunkRows, kTile, kThreads>(a, kChunkLeast, scratch);
+    const Run run = make_run<kChunkRows, kTile, kThreads, 1>(a, 0, kChunkLeast, scratch);
     if (threadIdx.x == 0) {
         for (int X = 0; X < 2; X++) {
             mbar_init(&sh.q_full[X], kSoft);
