@@ -7,12 +7,15 @@
 // element is used for at most 16 rows, so the weight's bytes are the floor and
 // the work beside them is turning E2M1 codes and E4M3 scales into operands.
 //
-// One CTA (8 warps) takes the 64 weight rows {32 i + 16 half + 0..15} of a
-// 128-row scale tile: there the tile layout puts the four scales of four such
-// rows into 16 consecutive bytes, so one 16-byte load serves four row groups.
-// The warps (and the CTAs of a cluster) split K in chunks of 128 columns.  In
-// a chunk lane (g, t) loads 16 bytes (32 consecutive columns, two scale
-// blocks) of rows g and g + 8 of each row group; the columns of the 16 x 8 x 16
+// One CTA an SM takes an equal share of the weight's groups of 16 rows.  Four
+// groups {32 i + 16 half + 0..15} of a 128-row scale tile make a quad: the tile
+// layout has the scales of four such rows in 16 consecutive bytes.  The 12 warps
+// split K in chunks of 128 columns, so a row of activations is read and scaled
+// once a warp and chunk for the up to 128 rows of a pass.  The weight's bytes
+// pass through a ring of three (quad, chunk) pieces in shared memory a warp,
+// which runs on across passes: 110 KB an SM on the way, and no registers wait.
+// In a piece lane (g, t) reads 16 bytes (32 consecutive columns, two scale
+// blocks) of rows g and g + 8 of each group; the columns of the 16 x 8 x 16
 // matrix instruction are permuted so that these are its own A fragments, and
 // the B fragments are 32 consecutive activations of row g.
 //
@@ -29,12 +32,15 @@ namespace gemv {
 
 using namespace fp4mma;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 64;         // weight rows of a CTA
-constexpr int kChunk = 128;       // columns a warp takes at a time
+constexpr int kSms = 148;
+constexpr int kChunk = 128;        // columns of a piece
+constexpr int kQuads = 2;          // quads of a pass
+constexpr int kStages = 3;         // of a warp's ring
+constexpr int kPiece = 64 * 64 + 2 * 16 * 16;  // a piece's codes, then its scales
 constexpr int kMaxM = 16;
-constexpr int kPitch = kRows + 4;  // of the partial sums' rows: the fragment stores spread over all banks
+constexpr int kPitch = 64 + 4;     // of the partial sums' rows: the fragment stores spread over all banks
 
 struct Args {
     const uint8_t* x;  // bf16 [m][ldx]
@@ -46,39 +52,57 @@ struct Args {
     const __nv_bfloat16 *bias, *mod_scale, *mod_shift, *gate, *residual;
     int64_t ldx, ldy, ld_res;
     int m, n, k, act;
-    int chunks, cluster;
-};
-
-// The chunk's weight bytes and activations of one lane.
-template <int NT>
-struct Loaded {
-    uint4 c[8];      // codes of rows 32 i + g and 32 i + g + 8, i = 0..3
-    uint4 s[2];      // scale bytes of the rows' tile: word i belongs to row group i
-    uint4 x[NT][4];  // 32 activations of row g of each row tile
+    int chunks, groups;
 };
 
 template <int NT>
-__device__ __forceinline__ void load_chunk(const Args& a, int row0, int c, int g, int t, Loaded<NT>& l) {
-    const int col = c * kChunk + 32 * t;
-    const bool in_k = col < a.k;  // k is a multiple of 64, so the lane's 32 columns are in or out as a whole
+constexpr int smem_bytes() {
+    return kWarps * (kStages * kPiece + 8 * NT * kPitch * 4);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+    return v;
+}
+
+// Quad q's groups 4 q + lo .. 4 q + hi - 1 belong to the CTA; its row 16 i + r
+// is row `row0` + 32 i + r of the weight.
+struct Quad {
+    int row0, lo, hi;
+    __device__ __forceinline__ Quad(int q, int g0, int g1) {
+        row0 = (q >> 1) * 128 + (q & 1) * 16;
+        lo = max(0, g0 - 4 * q);
+        hi = min(4, g1 - 4 * q);
+    }
+};
+
+// The piece (quad, chunk c) into a ring slot; what lies outside the weight or
+// belongs to another CTA's groups is not read (zeros).
+__device__ __forceinline__ void load_piece(const Args& a, const Quad& q, int c, int lane, uint32_t dst) {
     const int64_t pitch = a.k / 2;
-    const uint8_t* p = a.codes + (int64_t)(row0 + g) * pitch + col / 2;
+    const int part = lane & 3, r = lane >> 2, col = c * kChunk + 32 * part;
+    const bool in_k = col < a.k;  // k is a multiple of 64, so the lane's 32 columns are in or out as a whole
+    const uint8_t* p = a.codes + (int64_t)(q.row0 + r) * pitch + col / 2;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const int r = (i >> 1) * 32 + (i & 1) * 8;
-        l.c[i] = in_k && row0 + g + r < a.n ? ld_stream16(p + r * pitch) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    // tile (row0 / 128, col / 64); the tiles cover rows up to the next multiple of 128
-    const uint8_t* ps = a.scales + ((int64_t)(row0 >> 7) * (a.k / 64) + col / 64) * 512 + ((row0 & 31) + g) * 16;
+    for (int i = 0; i < 4; i++)
+        if (i >= q.lo && i < q.hi) {
 #pragma unroll
-    for (int h = 0; h < 2; h++) l.s[h] = in_k ? ld_stream16(ps + 128 * h) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int j = 0; j < NT; j++) {
-        const uint4* px = reinterpret_cast<const uint4*>(a.x + ((int64_t)(8 * j + g) * a.ldx + col) * 2);
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            l.x[j][i] = in_k && 8 * j + g < a.m ? __ldg(px + i) : make_uint4(0u, 0u, 0u, 0u);
-    }
+            for (int h = 0; h < 2; h++) {
+                const int row = 32 * i + 8 * h;
+                const bool real = in_k && q.row0 + r + row < a.n;
+                copy16(dst + (16 * i + 8 * h + r) * 64 + 16 * part, real ? p + row * pitch : a.codes, real);
+            }
+        }
+    // two scale tiles (64 columns each), 16 rows of 16 bytes; the tiles cover rows up to the next multiple of 128
+    const int tile = lane >> 4, tcol = c * kChunk + 64 * tile;
+    const bool real = tcol < a.k;
+    const uint8_t* ps = a.scales + ((int64_t)(q.row0 >> 7) * (a.k / 64) + tcol / 64) * 512 + ((q.row0 & 31) + (lane & 15)) * 16;
+    copy16(dst + 64 * 64 + tile * 256 + (lane & 15) * 16, real ? ps : a.scales, real);
 }
 
 // 32 codes of one row with their two block scales -> 16 operand pairs
@@ -96,103 +120,132 @@ __device__ __forceinline__ float act_gelu(float y) {
     return 0.5f * y * (1.0f + tanhf(u));
 }
 
-__device__ __forceinline__ float peer_f32(const float* p, uint32_t rank) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(p), rank)));
-    return v;
-}
-
 template <int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) gemv_kernel(const __grid_constant__ Args a) {
-    __shared__ float part[kWarps][8 * NT][kPitch];
+__global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant__ Args a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int rank = a.cluster == 1 ? 0 : (int)(blockIdx.x % (unsigned)a.cluster);
-    const int tile = (int)(blockIdx.x / (unsigned)a.cluster);
-    const int row0 = (tile >> 1) * 128 + (tile & 1) * 16;  // rows row0 + 32 i + 0..15
-    float acc[NT][4][4];
-#pragma unroll
-    for (int j = 0; j < NT; j++)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) acc[j][i][e] = 0.0f;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages * kPiece);
+    float(*part)[8 * NT][kPitch] = reinterpret_cast<float(*)[8 * NT][kPitch]>(smem + kWarps * kStages * kPiece);
+    // the CTA's groups [g0, g1) and their quads [first, last]
+    const int g0 = (int)((int64_t)a.groups * blockIdx.x / gridDim.x), g1 = (int)((int64_t)a.groups * (blockIdx.x + 1) / gridDim.x);
+    if (g0 >= g1) return;
+    const int first = g0 / 4, last = (g1 - 1) / 4;
 
-    const int step = kWarps * a.cluster;
-    for (int c = rank * kWarps + warp; c < a.chunks; c += step) {
-        Loaded<NT> l;
-        load_chunk<NT>(a, row0, c, g, t, l);
-        uint32_t xb[NT][16];
-        float inv[NT][2];
-#pragma unroll
-        for (int j = 0; j < NT; j++) {
-            const float back = scale_row<4>(l.x[j], xb[j]);
-            // the fragment's columns 2t, 2t + 1 are activation rows held by lanes (2t, .), (2t + 1, .)
-            inv[j][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * t);
-            inv[j][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint32_t s0 = i == 0 ? l.s[0].x : i == 1 ? l.s[0].y : i == 2 ? l.s[0].z : l.s[0].w;
-            const uint32_t s1 = i == 0 ? l.s[1].x : i == 1 ? l.s[1].y : i == 2 ? l.s[1].z : l.s[1].w;
-            uint32_t w0[16], w1[16];
-            decode32(l.c[2 * i], s0 >> (16 * (t & 1)), w0);
-            decode32(l.c[2 * i + 1], s1 >> (16 * (t & 1)), w1);
-#pragma unroll
-            for (int j = 0; j < NT; j++) {
-                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    mma_16816(d, w0[2 * e], w1[2 * e], w0[2 * e + 1], w1[2 * e + 1], xb[j][2 * e], xb[j][2 * e + 1]);
-#pragma unroll
-                for (int e = 0; e < 4; e++) acc[j][i][e] = fmaf(d[e], inv[j][e & 1], acc[j][i][e]);
+    // the next piece to fetch: pass by pass, chunk by chunk, quad by quad
+    int f_quad = first, f_pass = first, f_chunk = warp, f_slot = 0;
+    auto fetch = [&]() {
+        if (f_chunk < a.chunks && f_pass <= last) {
+            load_piece(a, Quad(f_quad, g0, g1), f_chunk, lane, ring + (uint32_t)(f_slot * kPiece));
+            f_slot = f_slot == kStages - 1 ? 0 : f_slot + 1;
+            if (++f_quad > min(last, f_pass + kQuads - 1)) {
+                f_chunk += kWarps;
+                if (f_chunk >= a.chunks) {
+                    f_chunk = warp;
+                    f_pass += kQuads;
+                }
+                f_quad = f_pass;
             }
         }
-    }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-    for (int j = 0; j < NT; j++)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                part[warp][8 * j + 2 * t + (e & 1)][16 * i + g + 8 * (e >> 1)] = acc[j][i][e];
-    __syncthreads();
-    // the warps' sums, then the cluster's, in a fixed order
-    const int outs = a.m * kRows;
-    if (a.cluster > 1) {
-        for (int o = threadIdx.x; o < outs; o += kThreads) {
-            const int n = o / kRows, r = o % kRows;
-            float s = part[0][n][r];
-#pragma unroll
-            for (int w = 1; w < kWarps; w++) s += part[w][n][r];
-            part[0][n][r] = s;
-        }
-        cluster_sync_all();
-    }
+    for (int i = 0; i < kStages - 1; i++) fetch();
+
     const float alpha = __ldg(a.a32);
-    const int share = (outs + a.cluster - 1) / a.cluster;
-    const int last = min(outs, (rank + 1) * share);
-    for (int o = rank * share + threadIdx.x; o < last; o += kThreads) {
-        const int m = o / kRows, r = o % kRows;
-        const int n = row0 + (r >> 4) * 32 + (r & 15);
-        float s = 0.0f;
-        if (a.cluster > 1) {
-            for (int q = 0; q < a.cluster; q++) s += peer_f32(&part[0][m][r], (uint32_t)q);
-        } else {
+    int slot = 0;
+    for (int pass = first; pass <= last; pass += kQuads) {
+        float acc[kQuads][NT][4][4];
 #pragma unroll
-            for (int w = 0; w < kWarps; w++) s += part[w][m][r];
+        for (int q = 0; q < kQuads; q++)
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) acc[q][j][i][e] = 0.0f;
+#pragma unroll 1
+        for (int c = warp; c < a.chunks; c += kWarps) {
+            uint32_t xb[NT][16];
+            float inv[NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+                uint4 raw[4];
+                const int col = c * kChunk + 32 * t;
+                const uint4* px = reinterpret_cast<const uint4*>(a.x + ((int64_t)(8 * j + g) * a.ldx + col) * 2);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    raw[i] = col < a.k && 8 * j + g < a.m ? __ldg(px + i) : make_uint4(0u, 0u, 0u, 0u);
+                const float back = scale_row<4>(raw, xb[j]);
+                // the fragment's columns 2t, 2t + 1 are activation rows held by lanes (2t, .), (2t + 1, .)
+                inv[j][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * t);
+                inv[j][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4);
+            }
+#pragma unroll
+            for (int q = 0; q < kQuads; q++) {
+                if (pass + q > last) continue;
+                const Quad quad(pass + q, g0, g1);
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+                __syncwarp();  // the piece is there for every lane, and every lane has left the slot that is filled next
+                fetch();
+                const uint32_t at = ring + (uint32_t)(slot * kPiece);
+                slot = slot == kStages - 1 ? 0 : slot + 1;
+                const uint32_t scales = at + 64 * 64 + (t >> 1) * 256 + g * 16;
+                const uint4 s0 = lds16(scales), s1 = lds16(scales + 8 * 16);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    if (i < quad.lo || i >= quad.hi) continue;
+                    const uint32_t codes = at + (16 * i + g) * 64 + 16 * t;
+                    uint32_t w0[16], w1[16];
+                    decode32(lds16(codes), (i == 0 ? s0.x : i == 1 ? s0.y : i == 2 ? s0.z : s0.w) >> (16 * (t & 1)), w0);
+                    decode32(lds16(codes + 8 * 64), (i == 0 ? s1.x : i == 1 ? s1.y : i == 2 ? s1.z : s1.w) >> (16 * (t & 1)),
+                             w1);
+#pragma unroll
+                    for (int j = 0; j < NT; j++) {
+                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            mma_16816(d, w0[2 * e], w1[2 * e], w0[2 * e + 1], w1[2 * e + 1], xb[j][2 * e],
+                                      xb[j][2 * e + 1]);
+#pragma unroll
+                        for (int e = 0; e < 4; e++) acc[q][j][i][e] = fmaf(d[e], inv[j][e & 1], acc[q][j][i][e]);
+                    }
+                }
+            }
         }
-        if (n >= a.n) continue;
-        float y = a.bias ? fmaf(alpha, s, __bfloat162float(a.bias[n])) : alpha * s;
-        if (a.act == NVFP4_ACT_GELU_TANH) y = act_gelu(y);
-        if (a.mod_scale) y = __fmul_rn(y, __fadd_rn(1.0f, __bfloat162float(a.mod_scale[n])));
-        if (a.mod_shift) y = __fadd_rn(y, __bfloat162float(a.mod_shift[n]));
-        if (a.gate) y = __fmul_rn(__bfloat162float(a.gate[n]), y);
-        if (a.residual) y = __fadd_rn(__bfloat162float(a.residual[(int64_t)m * a.ld_res + n]), y);
-        if (a.y) a.y[(int64_t)m * a.ldy + n] = __float2bfloat16_rn(y);
-        if (a.y32) a.y32[(int64_t)m * a.n + n] = y;
+        // the warps' sums, in a fixed order, and the epilogue
+#pragma unroll
+        for (int q = 0; q < kQuads; q++) {
+            if (pass + q > last) continue;
+            const Quad quad(pass + q, g0, g1);
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        part[warp][8 * j + 2 * t + (e & 1)][16 * i + g + 8 * (e >> 1)] = acc[q][j][i][e];
+            __syncthreads();
+            for (int o = threadIdx.x; o < a.m * 64; o += kThreads) {
+                const int m = o / 64, r = o % 64;
+                const int n = quad.row0 + (r >> 4) * 32 + (r & 15);
+                if ((r >> 4) < quad.lo || (r >> 4) >= quad.hi || n >= a.n) continue;
+                float s = part[0][m][r];
+#pragma unroll
+                for (int w = 1; w < kWarps; w++) s += part[w][m][r];
+                float y = a.bias ? fmaf(alpha, s, __bfloat162float(a.bias[n])) : alpha * s;
+                if (a.act == NVFP4_ACT_GELU_TANH) y = act_gelu(y);
+                if (a.mod_scale) y = __fmul_rn(y, __fadd_rn(1.0f, __bfloat162float(a.mod_scale[n])));
+                if (a.mod_shift) y = __fadd_rn(y, __bfloat162float(a.mod_shift[n]));
+                if (a.gate) y = __fmul_rn(__bfloat162float(a.gate[n]), y);
+                if (a.residual) y = __fadd_rn(__bfloat162float(a.residual[(int64_t)m * a.ld_res + n]), y);
+                if (a.y) a.y[(int64_t)m * a.ldy + n] = __float2bfloat16_rn(y);
+                if (a.y32) a.y32[(int64_t)m * a.n + n] = y;
+            }
+            __syncthreads();
+        }
     }
-    // a CTA's shared memory stays until every peer has read it
-    if (a.cluster > 1) cluster_sync_all();
 }
 
 }  // namespace gemv
@@ -247,23 +300,33 @@ extern "C" nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t m, int64_t ldx, c
     a.n = (int)n;
     a.k = (int)k;
     a.chunks = (int)((k + gemv::kChunk - 1) / gemv::kChunk);
-    // 64-row tiles: two a 128-row block (the second of the last block may be all padding rows)
-    const int64_t tiles = (n + 127) / 128 * 2;
-    // K is split over a cluster until two CTAs an SM (148 SMs) have work, as long as every warp keeps a chunk
-    a.cluster = 1;
-    while (a.cluster < 8 && tiles * a.cluster < 2 * 148 && a.chunks >= 2 * a.cluster * gemv::kWarps) a.cluster *= 2;
+    // groups of 16 rows, eight a 128-row scale tile (the last tile's may be padding)
+    a.groups = (int)((n + 127) / 128 * 8);
+    static PerDevice<int> ready;
+    int done = 0;
+    const nvfp4_status st = ready.get(&done, [](int, int& v) {
+        v = 1;
+        return cudaFuncSetAttribute(gemv::gemv_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    gemv::smem_bytes<1>()) == cudaSuccess &&
+                       cudaFuncSetAttribute(gemv::gemv_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            gemv::smem_bytes<2>()) == cudaSuccess
+                   ? NVFP4_OK
+                   : NVFP4_ERR_CUDA;
+    });
+    if (st != NVFP4_OK) return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * a.cluster));
+    cfg.gridDim = dim3((unsigned)(a.groups < gemv::kSms ? a.groups : gemv::kSms));
     cfg.blockDim = dim3(gemv::kThreads);
+    cfg.dynamicSmemBytes = (size_t)(m <= 8 ? gemv::smem_bytes<1>() : gemv::smem_bytes<2>());
     cfg.stream = (cudaStream_t)stream;
+    // programmatic dependent launch: the grid's start overlaps the previous kernel's end (the kernel waits for it
+    // before it reads anything)
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)a.cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, a.m <= 8 ? gemv::gemv_kernel<1> : gemv::gemv_kernel<2>, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, m <= 8 ? gemv::gemv_kernel<1> : gemv::gemv_kernel<2>, a) != cudaSuccess) {
         cudaGetLastError();
         return NVFP4_ERR_CUDA;
     }

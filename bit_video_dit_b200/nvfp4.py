@@ -353,17 +353,25 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, *, out: torch.Tensor | None = None, bia
     return out
 
 
+# The current stream's handle by device index; torch.cuda.current_stream() makes an object each time, which takes
+# longer than the rest of a small call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch_on(device: torch.device, stream, fn, *args) -> int:
     """Call fn(*args, stream) with `device` current (its current stream when none is given)."""
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream(stream))
+    raw = _raw_stream(device.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, raw)
     with torch.cuda.device(device):
-        return fn(*args, _stream(stream))
+        return fn(*args, raw)
 
 
 def _same_device(device: torch.device, *ts) -> None:
+    index = device.index
     for t in ts:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"every tensor of the call has to be on {device}")
 
 
@@ -374,14 +382,15 @@ def gemv(x: torch.Tensor, w: NVFP4Tensor, *, out: torch.Tensor | None = None, ou
     quantized, then gemm's epilogue (bias, act, modulate, gate, residual); bf16 `out` [M, N] (rows may be strided)
     and, when out_f32 is given, the same in float32 before the store."""
     _require_cuda(x)
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1 or x.shape[1] != w.cols:
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != w.cols or x.stride(1) != 1:
         raise ValueError("gemv takes bf16 x [M, K] with unit column stride and K of the weight")
     M, N = x.shape[0], w.rows
+    device = x.device
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=device)
     elif out.dtype != torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1:
         raise ValueError("out is bf16 [M, N] with unit column stride")
-    _same_device(x.device, w.codes, out, out_f32, bias, mod_scale, mod_shift, gate, residual)
+    _same_device(device, w.codes, out, out_f32, bias, mod_scale, mod_shift, gate, residual)
     ep = None
     if act or not (bias is mod_scale is mod_shift is gate is residual is out_f32 is None):
         for v in (bias, mod_scale, mod_shift, gate):
@@ -397,8 +406,9 @@ def gemv(x: torch.Tensor, w: NVFP4Tensor, *, out: torch.Tensor | None = None, ou
                                         residual=residual, act=act, debug_y=out_f32))
     # a row stride means nothing for a single row
     ldx, ldy = (x.stride(0), out.stride(0)) if M > 1 else (w.cols, N)
-    _check("nvfp4_gemv", _launch_on(x.device, stream, lib().nvfp4_gemv, x.data_ptr(), M, ldx, ctypes.byref(w.c()),
-                                    out.data_ptr(), ldy, ep))
+    st = _launch_on(device, stream, lib().nvfp4_gemv, x.data_ptr(), M, ldx, ctypes.byref(w.c()), out.data_ptr(), ldy, ep)
+    if st:
+        _check("nvfp4_gemv", st)
     return out
 
 
@@ -503,7 +513,8 @@ class PagedRows:
     """The sequences of a step (nvfp4_paged_rows): sequence b owns rows row_start[b] .. row_start[b + 1] - 1 of the
     step's row tensors, which are its last positions, lens[b] - n_b .. lens[b] - 1; pages[b] lists its cache pages.
     Contiguous device int32 tensors [B + 1], [B] and [B, max_pages], read by the kernels at every call; n_rows (rows
-    of the row tensors), max_rows (most rows of a sequence) and max_len (longest sequence) are the host's bounds."""
+    of the row tensors), max_rows (most rows of a sequence) and max_len (longest sequence) are the host's bounds.
+    Change the tensors in place; another one makes another PagedRows."""
 
     def __init__(self, row_start: torch.Tensor, lens: torch.Tensor, pages: torch.Tensor, *, n_rows: int, max_rows: int,
                  max_len: int):
@@ -519,6 +530,7 @@ class PagedRows:
         self.n_seqs, self.n_rows, self.max_rows, self.max_len = B, n_rows, max_rows, max_len
         self._c = CPagedRows(row_start.data_ptr(), lens.data_ptr(), pages.data_ptr(), B, pages.shape[1], n_rows,
                              max_rows, max_len)
+        self._ref = ctypes.byref(self._c)
 
     def c(self) -> CPagedRows:
         return self._c
@@ -528,7 +540,7 @@ class PagedKVCache:
     """NVFP4 cache of n_pages pages of page_size tokens x kv_heads x head_dim (64 or 128) for sequences that grow by
     tokens: codes [n_pages, kv_heads, page_size, d / 2] and E4M3 scales [.., d / 16] of K and V, under one tensor
     scale each for the whole cache (k_scale, v_scale: numbers or device float32 tensors; amax / 2688 of a
-    calibration).  The caller hands out the pages."""
+    calibration).  The caller hands out the pages.  The cache's tensors are its own for its life: fill them in place."""
 
     def __init__(self, n_pages: int, page_size: int, kv_heads: int, head_dim: int, *, k_scale, v_scale, device="cuda"):
         self.n_pages, self.page_size, self.kv_heads, self.head_dim = n_pages, page_size, kv_heads, head_dim
@@ -546,6 +558,7 @@ class PagedKVCache:
         self._c = CPagedCache(self.k_codes.data_ptr(), self.k_scales.data_ptr(), self.v_codes.data_ptr(),
                               self.v_scales.data_ptr(), self.k_global.data_ptr(), self.v_global.data_ptr(), n_pages,
                               page_size, kv_heads, head_dim)
+        self._ref = ctypes.byref(self._c)
 
     def c(self) -> CPagedCache:
         return self._c
@@ -554,31 +567,39 @@ class PagedKVCache:
         return sum(t.numel() * t.element_size() for t in
                    (self.k_codes, self.v_codes, self.k_scales, self.v_scales, self.k_global, self.v_global))
 
-    def _check_rows(self, rows: PagedRows, heads: int, what: str, *ts) -> None:
-        _same_device(self.device, rows.lens, *ts)
+    def _row_strides(self, rows: PagedRows, heads: int, *ts) -> list[int]:
+        """Elements between the rows of [n_rows, heads, head_dim] tensors, which have to be fit for the call."""
+        index, d, shape, lds = self.device.index, self.head_dim, (rows.n_rows, heads, self.head_dim), []
+        if rows.lens.get_device() != index:
+            raise ValueError(f"the rows have to be on {self.device}")
         for t in ts:
-            if t.dtype != torch.bfloat16 or t.shape != (rows.n_rows, heads, self.head_dim) or (
-                    t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.head_dim))):
-                raise ValueError(f"{what} takes bf16 [n_rows, {heads}, {self.head_dim}] rows whose heads are contiguous")
-
-    def _ld(self, t: torch.Tensor) -> int:
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * self.head_dim
+            if t.get_device() != index:
+                raise ValueError(f"every tensor of the call has to be on {self.device}")
+            if t.dtype != torch.bfloat16 or t.shape != shape:
+                raise ValueError(f"row tensors are bf16 {list(shape)}: got {t.dtype} {list(t.shape)}")
+            ld, per_head, unit = t.stride()
+            if (unit != 1 or (per_head != d and heads > 1)) and rows.n_rows:
+                raise ValueError("the heads of a row have to be contiguous")
+            lds.append(ld if rows.n_rows > 1 else heads * d)  # a row stride means nothing for a single row
+        return lds
 
     def append(self, rows: PagedRows, k: torch.Tensor, v: torch.Tensor, *, rope=None, ws: torch.Tensor | None = None,
                stream=None) -> None:
         """Quantize the rows' K and V (bf16 [n_rows, kv_heads, d], rows may be strided) into their pages.  rope =
         (cos, sin), float32 [n_rows, d / 2] each: the keys are turned first (interleaved pairs, as KVCache.append)."""
-        self._check_rows(rows, self.kv_heads, "append", k, v)
-        cos, sin = rope if rope is not None else (None, None)
-        for t in (cos, sin):
-            if rope is not None and (t.dtype != torch.float32 or not t.is_contiguous() or
-                                     t.shape != (rows.n_rows, self.head_dim // 2)):
-                raise ValueError("rope tables are contiguous float32 [n_rows, d / 2]")
-        _same_device(self.device, cos, sin)
+        ld_k, ld_v = self._row_strides(rows, self.kv_heads, k, v)
+        cos = sin = None
+        if rope is not None:
+            cos, sin = rope
+            for t in rope:
+                if t.dtype != torch.float32 or t.shape != (rows.n_rows, self.head_dim // 2) or not t.is_contiguous():
+                    raise ValueError("rope tables are contiguous float32 [n_rows, d / 2]")
+            _same_device(self.device, cos, sin)
         ws = self.ws_rows if ws is None else ws
-        _check("nvfp4_paged_append", _launch_on(
-            self.device, stream, lib().nvfp4_paged_append, ctypes.byref(self._c), ctypes.byref(rows._c), k.data_ptr(),
-            self._ld(k), v.data_ptr(), self._ld(v), _ptr(cos), _ptr(sin), ws.data_ptr(), ws.numel()))
+        st = _launch_on(self.device, stream, lib().nvfp4_paged_append, self._ref, rows._ref, k.data_ptr(), ld_k,
+                        v.data_ptr(), ld_v, _ptr(cos), _ptr(sin), ws.data_ptr(), ws.numel())
+        if st:
+            _check("nvfp4_paged_append", st)
 
     def gather(self, rows: PagedRows, *, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
                ws: torch.Tensor | None = None, stream=None):
@@ -588,17 +609,17 @@ class PagedKVCache:
             k_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
         if v_out is None:
             v_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        self._check_rows(rows, self.kv_heads, "gather", k_out, v_out)
+        ld_k, ld_v = self._row_strides(rows, self.kv_heads, k_out, v_out)
         ws = self.ws_rows if ws is None else ws
-        _check("nvfp4_paged_gather", _launch_on(
-            self.device, stream, lib().nvfp4_paged_gather, ctypes.byref(self._c), ctypes.byref(rows._c),
-            k_out.data_ptr(), self._ld(k_out), v_out.data_ptr(), self._ld(v_out), ws.data_ptr(), ws.numel()))
+        st = _launch_on(self.device, stream, lib().nvfp4_paged_gather, self._ref, rows._ref, k_out.data_ptr(), ld_k,
+                        v_out.data_ptr(), ld_v, ws.data_ptr(), ws.numel())
+        if st:
+            _check("nvfp4_paged_gather", st)
         return k_out, v_out
 
     def attention_workspace(self, rows: PagedRows, heads: int, *, window: int = 0, sinks: int = 0) -> torch.Tensor:
         """A workspace for attention() with these arguments (and for any with fewer rows of the same bounds)."""
-        n = int(lib().nvfp4_paged_attention_workspace_bytes(ctypes.byref(self._c), ctypes.byref(rows._c), heads, window,
-                                                            sinks))
+        n = int(lib().nvfp4_paged_attention_workspace_bytes(self._ref, rows._ref, heads, window, sinks))
         if n == 0:
             raise ValueError("nvfp4_paged_attention_workspace_bytes: refused arguments")
         ws = torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -614,13 +635,13 @@ class PagedKVCache:
         heads = q.shape[1]
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        self._check_rows(rows, heads, "attention", q, out)
+        ld_q, ld_o = self._row_strides(rows, heads, q, out)
         if ws is None:
             ws = self.attention_workspace(rows, heads, window=window, sinks=sinks)
-        _check("nvfp4_paged_attention", _launch_on(
-            self.device, stream, lib().nvfp4_paged_attention, ctypes.byref(self._c), ctypes.byref(rows._c),
-            q.data_ptr(), self._ld(q), heads, window, sinks, scale, out.data_ptr(), self._ld(out), ws.data_ptr(),
-            ws.numel()))
+        st = _launch_on(self.device, stream, lib().nvfp4_paged_attention, self._ref, rows._ref, q.data_ptr(), ld_q,
+                        heads, window, sinks, scale, out.data_ptr(), ld_o, ws.data_ptr(), ws.numel())
+        if st:
+            _check("nvfp4_paged_attention", st)
         return out
 
 
