@@ -9,20 +9,22 @@
 //
 // One CTA an SM takes an equal share of the weight's groups of 16 rows.  Four
 // groups {32 i + 16 half + 0..15} of a 128-row scale tile make a quad: the tile
-// layout has the scales of four such rows in 16 consecutive bytes.  The 12 warps
-// split K in chunks of 128 columns, so a row of activations is read and scaled
-// once a warp and chunk for the up to 128 rows of a pass.  The weight's bytes
-// pass through a ring of three (quad, chunk) pieces in shared memory a warp,
-// which runs on across passes: 110 KB an SM on the way, and no registers wait.
+// layout has the scales of four such rows in 16 consecutive bytes.  The warps
+// split K in chunks of 128 columns and take two or three quads of rows at a time,
+// so that a chunk's activations serve 128 rows.  The weight's bytes pass
+// through a ring of (quad, chunk) pieces in shared memory a warp, which runs on
+// across passes: 70 to 110 KB an SM on the way, and no registers wait.
 // In a piece lane (g, t) reads 16 bytes (32 consecutive columns, two scale
 // blocks) of rows g and g + 8 of each group; the columns of the 16 x 8 x 16
 // matrix instruction are permuted so that these are its own A fragments, and
 // the B fragments are 32 consecutive activations of row g.
 //
 // Operands: e2m1 * s is exact in binary16 (at most 6 significant bits); a row
-// of activations is scaled by a power of two per chunk and rounded to binary16
-// (fp4mma.cuh), and the power comes off in the binary32 accumulation over the
-// chunks.
+// of activations is scaled by a power of two and rounded to binary16
+// (fp4mma.cuh).  When all of them fit, the scaled activations lie in shared
+// memory and the power comes off at the end; else a chunk's activations pass
+// through the ring before its pieces and have a power of their own, which comes
+// off the chunk's sums.
 #include <cstdint>
 
 #include "fp4mma.cuh"
@@ -32,15 +34,21 @@ namespace gemv {
 
 using namespace fp4mma;
 
-constexpr int kWarps = 12;
-constexpr int kThreads = kWarps * 32;
 constexpr int kSms = 148;
-constexpr int kChunk = 128;        // columns of a piece
-constexpr int kQuads = 2;          // quads of a pass
-constexpr int kStages = 3;         // of a warp's ring
+constexpr int kChunk = 128;  // columns of a piece
 constexpr int kPiece = 64 * 64 + 2 * 16 * 16;  // a piece's codes, then its scales
 constexpr int kMaxM = 16;
-constexpr int kPitch = 64 + 4;     // of the partial sums' rows: the fragment stores spread over all banks
+constexpr int kPitch = 64 + 4;  // of the partial sums' rows: the fragment stores spread over all banks
+
+// Up to 8 rows (NT = 1): 16 warps of 128 registers, two pieces a ring; up to 16
+// rows: 12 of 168, three pieces.  (What the accumulators leave room for.)
+template <int NT>
+struct Cfg {
+    static constexpr int kWarps = NT == 1 ? 16 : 12, kThreads = kWarps * 32, kStages = NT == 1 ? 2 : 3;
+    static constexpr int kQuads = NT == 1 ? 3 : 2;  // of a pass
+    static constexpr int kRing = kWarps * kStages * kPiece, kPart = kWarps * 8 * NT * kPitch * 4;
+    static constexpr int kX = 227 * 1024 - 256 - kRing - kPart;  // what is left for activations
+};
 
 struct Args {
     const uint8_t* x;  // bf16 [m][ldx]
@@ -54,11 +62,6 @@ struct Args {
     int m, n, k, act;
     int chunks, groups;
 };
-
-template <int NT>
-constexpr int smem_bytes() {
-    return kWarps * (kStages * kPiece + 8 * NT * kPitch * 4);
-}
 
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
@@ -81,28 +84,51 @@ struct Quad {
     }
 };
 
-// The piece (quad, chunk c) into a ring slot; what lies outside the weight or
-// belongs to another CTA's groups is not read (zeros).
+// The piece (quad, chunk c) into a ring slot; what lies outside the weight is
+// zeros, and groups of other CTAs are not read.
 __device__ __forceinline__ void load_piece(const Args& a, const Quad& q, int c, int lane, uint32_t dst) {
     const int64_t pitch = a.k / 2;
     const int part = lane & 3, r = lane >> 2, col = c * kChunk + 32 * part;
     const bool in_k = col < a.k;  // k is a multiple of 64, so the lane's 32 columns are in or out as a whole
     const uint8_t* p = a.codes + (int64_t)(q.row0 + r) * pitch + col / 2;
+    const uint32_t d = dst + r * 64 + 16 * part;
+    if (q.row0 + 112 <= a.n && (c + 1) * kChunk <= a.k) {
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-        if (i >= q.lo && i < q.hi) {
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int row = 32 * i + 8 * h;
-                const bool real = in_k && q.row0 + r + row < a.n;
-                copy16(dst + (16 * i + 8 * h + r) * 64 + 16 * part, real ? p + row * pitch : a.codes, real);
+        for (int i = 0; i < 4; i++, p += 32 * pitch)
+            if (i >= q.lo && i < q.hi) {
+                copy16(d + 16 * i * 64, p, true);
+                copy16(d + (16 * i + 8) * 64, p + 8 * pitch, true);
             }
-        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (i >= q.lo && i < q.hi) {
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int row = 32 * i + 8 * h;
+                    const bool real = in_k && q.row0 + r + row < a.n;
+                    copy16(d + (16 * i + 8 * h) * 64, real ? p + row * pitch : a.codes, real);
+                }
+            }
+    }
     // two scale tiles (64 columns each), 16 rows of 16 bytes; the tiles cover rows up to the next multiple of 128
     const int tile = lane >> 4, tcol = c * kChunk + 64 * tile;
     const bool real = tcol < a.k;
     const uint8_t* ps = a.scales + ((int64_t)(q.row0 >> 7) * (a.k / 64) + tcol / 64) * 512 + ((q.row0 & 31) + (lane & 15)) * 16;
-    copy16(dst + 64 * 64 + tile * 256 + (lane & 15) * 16, real ? ps : a.scales, real);
+    copy16(dst + 64 * 64 + lane * 16, real ? ps : a.scales, real);
+}
+
+// Where 16-byte piece j (8 values) of a chunk's row r lies among the row's 16:
+// the four lanes of two rows then read eight different bank groups.
+__device__ __forceinline__ int x_place(int r, int j) { return (j & ~3) | ((j ^ (j >> 2) ^ (r & 1)) & 3); }
+
+// A chunk's activations (bf16) into a ring slot, the pieces of a row placed as above; columns behind K are zeros.
+__device__ __forceinline__ void load_x(const Args& a, int c, int lane, uint32_t dst) {
+    for (int i = lane; i < a.m * 16; i += 32) {
+        const int m = i >> 4, j = i & 15, col = c * kChunk + 8 * j;
+        const bool real = col < a.k;
+        copy16(dst + m * 256 + x_place(m, j) * 16, real ? a.x + ((int64_t)m * a.ldx + col) * 2 : a.x, real);
+    }
 }
 
 // 32 codes of one row with their two block scales -> 16 operand pairs
@@ -120,24 +146,30 @@ __device__ __forceinline__ float act_gelu(float y) {
     return 0.5f * y * (1.0f + tanhf(u));
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant__ Args a) {
+template <int NT, bool XS>
+__global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) gemv_kernel(const __grid_constant__ Args a) {
+    constexpr int kWarps = Cfg<NT>::kWarps, kThreads = Cfg<NT>::kThreads, kStages = Cfg<NT>::kStages, kQuads = Cfg<NT>::kQuads;
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t row_max[kMaxM];
     asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages * kPiece);
-    float(*part)[8 * NT][kPitch] = reinterpret_cast<float(*)[8 * NT][kPitch]>(smem + kWarps * kStages * kPiece);
+    float(*part)[8 * NT][kPitch] = reinterpret_cast<float(*)[8 * NT][kPitch]>(smem + Cfg<NT>::kRing);
+    const uint32_t xs = smem_u32(smem) + Cfg<NT>::kRing + Cfg<NT>::kPart;
+    if (threadIdx.x < kMaxM) row_max[threadIdx.x] = 0u;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // the CTA's groups [g0, g1) and their quads [first, last]
     const int g0 = (int)((int64_t)a.groups * blockIdx.x / gridDim.x), g1 = (int)((int64_t)a.groups * (blockIdx.x + 1) / gridDim.x);
     if (g0 >= g1) return;
     const int first = g0 / 4, last = (g1 - 1) / 4;
 
-    // the next piece to fetch: pass by pass, chunk by chunk, quad by quad
-    int f_quad = first, f_pass = first, f_chunk = warp, f_slot = 0;
+    // the next piece to fetch: pass by pass, chunk by chunk, (the chunk's activations, then) quad by quad
+    constexpr int kBefore = XS ? 0 : 1;
+    int f_quad = first - kBefore, f_pass = first, f_chunk = warp, f_slot = 0;
     auto fetch = [&]() {
         if (f_chunk < a.chunks && f_pass <= last) {
-            load_piece(a, Quad(f_quad, g0, g1), f_chunk, lane, ring + (uint32_t)(f_slot * kPiece));
+            if (!XS && f_quad < f_pass) load_x(a, f_chunk, lane, ring + (uint32_t)(f_slot * kPiece));
+            else load_piece(a, Quad(f_quad, g0, g1), f_chunk, lane, ring + (uint32_t)(f_slot * kPiece));
             f_slot = f_slot == kStages - 1 ? 0 : f_slot + 1;
             if (++f_quad > min(last, f_pass + kQuads - 1)) {
                 f_chunk += kWarps;
@@ -145,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
                     f_chunk = warp;
                     f_pass += kQuads;
                 }
-                f_quad = f_pass;
+                f_quad = f_pass - kBefore;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -153,8 +185,47 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < kStages - 1; i++) fetch();
 
+    float down[NT][2];  // what the sums' columns 2t, 2t + 1 are multiplied by
+    if (XS) {
+        // the rows' largest magnitudes, then the scaled rows
+        __syncthreads();
+        for (int m = 0; m < a.m; m++) {
+            const uint4* row = reinterpret_cast<const uint4*>(a.x + (int64_t)m * a.ldx * 2);
+            uint32_t mx = 0u;
+            for (int i = threadIdx.x; i < a.k / 8; i += kThreads) {
+                const uint4 v = __ldg(row + i);
+                mx = max(mx, max_bits<1>(&v));
+            }
+            mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+            if (lane == 0) atomicMax(&row_max[m], mx);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) down[j][e] = row_scale(row_max[8 * j + 2 * t + e]).down;
+        for (int m = 0; m < a.m; m++) {
+            const uint4* row = reinterpret_cast<const uint4*>(a.x + (int64_t)m * a.ldx * 2);
+            const float u = row_scale(row_max[m]).up;
+            for (int i = threadIdx.x; i < a.chunks * 16; i += kThreads) {
+                uint32_t h[4];
+                scale8(i < a.k / 8 ? __ldg(row + i) : make_uint4(0u, 0u, 0u, 0u), u, h);
+                st_shared16(xs + ((i >> 4) * a.m + m) * 256 + x_place(m, i & 15) * 16, make_uint4(h[0], h[1], h[2], h[3]));
+            }
+        }
+        __syncthreads();
+    }
+
     const float alpha = __ldg(a.a32);
     int slot = 0;
+    auto next_piece = [&]() {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncwarp();  // the piece is there for every lane, and every lane has left the slot that is filled next
+        fetch();
+        const uint32_t at = ring + (uint32_t)(slot * kPiece);
+        slot = slot == kStages - 1 ? 0 : slot + 1;
+        return at;
+    };
     for (int pass = first; pass <= last; pass += kQuads) {
         float acc[kQuads][NT][4][4];
 #pragma unroll
@@ -167,30 +238,29 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
                     for (int e = 0; e < 4; e++) acc[q][j][i][e] = 0.0f;
 #pragma unroll 1
         for (int c = warp; c < a.chunks; c += kWarps) {
-            uint32_t xb[NT][16];
-            float inv[NT][2];
+            // (columns of the product that are no row of x hold anything: nobody reads them)
+            uint32_t xb[NT][16], px = xs + c * a.m * 256;
+            if (!XS) px = next_piece();
 #pragma unroll
             for (int j = 0; j < NT; j++) {
-                uint4 raw[4];
-                const int col = c * kChunk + 32 * t;
-                const uint4* px = reinterpret_cast<const uint4*>(a.x + ((int64_t)(8 * j + g) * a.ldx + col) * 2);
+                const int m = min(8 * j + g, a.m - 1);
+                uint4 v[4];
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    raw[i] = col < a.k && 8 * j + g < a.m ? __ldg(px + i) : make_uint4(0u, 0u, 0u, 0u);
-                const float back = scale_row<4>(raw, xb[j]);
-                // the fragment's columns 2t, 2t + 1 are activation rows held by lanes (2t, .), (2t + 1, .)
-                inv[j][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * t);
-                inv[j][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4);
+                for (int i = 0; i < 4; i++) {
+                    v[i] = lds16(px + m * 256 + x_place(m, 4 * t + i) * 16);
+                    if (XS) xb[j][4 * i] = v[i].x, xb[j][4 * i + 1] = v[i].y, xb[j][4 * i + 2] = v[i].z, xb[j][4 * i + 3] = v[i].w;
+                }
+                if (!XS) {  // a scale for the chunk; columns 2t, 2t + 1 are rows of lanes (2t, .), (2t + 1, .)
+                    const float back = scale_row<4>(v, xb[j]);
+                    down[j][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * t);
+                    down[j][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4);
+                }
             }
 #pragma unroll
             for (int q = 0; q < kQuads; q++) {
                 if (pass + q > last) continue;
                 const Quad quad(pass + q, g0, g1);
-                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-                __syncwarp();  // the piece is there for every lane, and every lane has left the slot that is filled next
-                fetch();
-                const uint32_t at = ring + (uint32_t)(slot * kPiece);
-                slot = slot == kStages - 1 ? 0 : slot + 1;
+                const uint32_t at = next_piece();
                 const uint32_t scales = at + 64 * 64 + (t >> 1) * 256 + g * 16;
                 const uint4 s0 = lds16(scales), s1 = lds16(scales + 8 * 16);
 #pragma unroll
@@ -203,13 +273,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
                              w1);
 #pragma unroll
                     for (int j = 0; j < NT; j++) {
-                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        float chunk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        float* d = XS ? acc[q][j][i] : chunk;
 #pragma unroll
                         for (int e = 0; e < 8; e++)
                             mma_16816(d, w0[2 * e], w1[2 * e], w0[2 * e + 1], w1[2 * e + 1], xb[j][2 * e],
                                       xb[j][2 * e + 1]);
+                        if (!XS)
 #pragma unroll
-                        for (int e = 0; e < 4; e++) acc[q][j][i][e] = fmaf(d[e], inv[j][e & 1], acc[q][j][i][e]);
+                            for (int e = 0; e < 4; e++) acc[q][j][i][e] = fmaf(d[e], down[j][e & 1], acc[q][j][i][e]);
                     }
                 }
             }
@@ -225,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
                 for (int i = 0; i < 4; i++)
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        part[warp][8 * j + 2 * t + (e & 1)][16 * i + g + 8 * (e >> 1)] = acc[q][j][i][e];
+                        part[warp][8 * j + 2 * t + (e & 1)][16 * i + g + 8 * (e >> 1)] =
+                            XS ? acc[q][j][i][e] * down[j][e & 1] : acc[q][j][i][e];
             __syncthreads();
             for (int o = threadIdx.x; o < a.m * 64; o += kThreads) {
                 const int m = o / 64, r = o % 64;
@@ -306,18 +379,22 @@ extern "C" nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t m, int64_t ldx, c
     int done = 0;
     const nvfp4_status st = ready.get(&done, [](int, int& v) {
         v = 1;
-        return cudaFuncSetAttribute(gemv::gemv_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    gemv::smem_bytes<1>()) == cudaSuccess &&
-                       cudaFuncSetAttribute(gemv::gemv_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            gemv::smem_bytes<2>()) == cudaSuccess
-                   ? NVFP4_OK
-                   : NVFP4_ERR_CUDA;
+        const void* kernels[4] = {(const void*)gemv::gemv_kernel<1, false>, (const void*)gemv::gemv_kernel<1, true>,
+                                  (const void*)gemv::gemv_kernel<2, false>, (const void*)gemv::gemv_kernel<2, true>};
+        for (const void* f : kernels)
+            if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 256) != cudaSuccess)
+                return NVFP4_ERR_CUDA;
+        return NVFP4_OK;
     });
     if (st != NVFP4_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.groups < gemv::kSms ? a.groups : gemv::kSms));
-    cfg.blockDim = dim3(gemv::kThreads);
-    cfg.dynamicSmemBytes = (size_t)(m <= 8 ? gemv::smem_bytes<1>() : gemv::smem_bytes<2>());
+    const bool two = m > 8;
+    const int64_t xbytes = (int64_t)a.chunks * m * 256, room = two ? gemv::Cfg<2>::kX : gemv::Cfg<1>::kX;
+    const bool xs = xbytes <= room;
+    cfg.blockDim = dim3((unsigned)(two ? gemv::Cfg<2>::kThreads : gemv::Cfg<1>::kThreads));
+    cfg.dynamicSmemBytes = (size_t)((two ? gemv::Cfg<2>::kRing + gemv::Cfg<2>::kPart
+                                         : gemv::Cfg<1>::kRing + gemv::Cfg<1>::kPart) + (xs ? xbytes : 0));
     cfg.stream = (cudaStream_t)stream;
     // programmatic dependent launch: the grid's start overlaps the previous kernel's end (the kernel waits for it
     // before it reads anything)
@@ -326,7 +403,10 @@ extern "C" nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t m, int64_t ldx, c
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, m <= 8 ? gemv::gemv_kernel<1> : gemv::gemv_kernel<2>, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg,
+                           two ? (xs ? gemv::gemv_kernel<2, true> : gemv::gemv_kernel<2, false>)
+                               : (xs ? gemv::gemv_kernel<1, true> : gemv::gemv_kernel<1, false>),
+                           a) != cudaSuccess) {
         cudaGetLastError();
         return NVFP4_ERR_CUDA;
     }
