@@ -102,9 +102,9 @@ __device__ __forceinline__ bool group_seen(const Span& s, int k0) {
 // ---------------------------------------------------------------------------
 // The kernel for chunks (paged_attention.cu).
 constexpr int kChunkRows = 256;  // (row, query head) pairs of a unit
-constexpr int kChunkKeys = 128;
+constexpr int kChunkKeys = 64;
 constexpr int kChunkCtas = 148;  // one an SM
-constexpr int kChunkLeast = 2;   // tiles of a run
+constexpr int kChunkLeast = 4;   // tiles of a run
 struct AttnArgs;
 nvfp4_status launch_chunks(const AttnArgs& a, unsigned ctas, cudaStream_t stream);
 
@@ -166,7 +166,7 @@ struct Run {
 // What beginning and ending a unit costs, in tiles: a unit counts as that many
 // more, so that runs of short units are no longer than the others.
 template <int COLS>
-constexpr int kUnitCost = COLS == kChunkRows ? 1 : 5;
+constexpr int kUnitCost = COLS == kChunkRows ? 4 : 5;
 
 // Tiles of pair j as counted in the list (0: no rows), and as they are.
 template <int COLS, int T>
