@@ -526,6 +526,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Shared sh;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     RunScratch<kThreads>& scratch = *reinterpret_cast<RunScratch<kThreads>*>(smem);  // before the operands are there
     const int warp = threadIdx.x >> 5;
     const Run run = make_run<kChunkRows, kKeys, kThreads, 1>(a, 0, kChunkLeast, scratch);

@@ -166,6 +166,24 @@ def test_append_and_gather(d, page, heads, rope):
     assert torch.all(wide[owned:] == 3.0)
 
 
+def test_rows_aligned_to_16_bytes_only():
+    """Rows 8 elements apart from a 32-byte boundary, as slices of an oddly padded projection may be."""
+    require_gpu()
+    s = Setup([40, 9], [40, 3], 2, 64, 16, seed=31)
+    wide = torch.full((43, 3 * 128 + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    kb, vb = syn.normal_bf16((43, 2, 64), seed=1), syn.normal_bf16((43, 2, 64), seed=2)
+    k, v = wide[:, 8:136].unflatten(1, (2, 64)), wide[:, 136:264].unflatten(1, (2, 64))
+    k.copy_(dev_bf16(kb)), v.copy_(dev_bf16(vb))
+    s.cache.append(s.rows(), k, v)
+    k.fill_(0), v.fill_(0)
+    s.cache.gather(s.rows(), k_out=k, v_out=v)
+    s.check()
+    for got, bits, a in ((k, kb, K_SCALE), (v, vb, V_SCALE)):
+        want = oracle.dequant_bf16(*oracle.quantize(bits.reshape(-1, 64), alpha=a)).reshape(bits.shape)
+        assert np.array_equal(host_bits(got), want)
+    assert torch.all(wide[:, :8] == 3.0) and torch.all(wide[:, 264:] == 3.0)
+
+
 def test_rows_before_the_first_position_and_many_sequences():
     """More rows than positions: nothing is written for the rows before the first, and they read as zeros.  Hundreds of
     sequences, most without rows, find their rows."""
