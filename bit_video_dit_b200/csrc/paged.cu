@@ -289,33 +289,34 @@ __device__ __forceinline__ void load_tile(const View& v, const CopyLane<D>& ln, 
         const int at = v.page_shift >= 0 ? kq & (v.page_size - 1) : kq % v.page_size;
         row[q] = ok[q] ? (uint32_t)pages[q] * page_rows + head_row + (uint32_t)at : 0u;  // below 2^32 (host)
     }
-    if (ok[0] && ok[1] && k0 + kKeys <= sp.hi) {
 #pragma unroll
-        for (int q = 0; q < 2; q++) {
-            const uint8_t *k = ln.k + (uint64_t)row[q] * (D / 2), *w = ln.v + (uint64_t)row[q] * (D / 2);
+    for (int q = 0; q < 2; q++) {
+        const uint8_t *k = ln.k + (uint64_t)row[q] * (D / 2), *w = ln.v + (uint64_t)row[q] * (D / 2);
 #pragma unroll
-            for (int j = 0; j < 16 / kRows; j++) {
-                copy16(dst + ln.dk + (16 * q + j * kRows) * (D / 2), k + j * kRows * (D / 2), 16);
-                copy16(dst + ln.dv + (16 * q + j * kRows) * (D / 2), w + j * kRows * (D / 2), 16);
-            }
-        }
-        if (ln.scales) copy16(dst + ln.ds, ln.s + (uint64_t)(ln.skey < 16 ? row[0] : row[1]) * (D / 16), 16);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 2; q++) {
-            const uint8_t *k = ln.k + (uint64_t)row[q] * (D / 2), *w = ln.v + (uint64_t)row[q] * (D / 2);
-#pragma unroll
-            for (int j = 0; j < 16 / kRows; j++) {
-                const int n = ok[q] && k0 + 16 * q + j * kRows + ln.key < sp.hi ? 16 : 0;
-                copy16(dst + ln.dk + (16 * q + j * kRows) * (D / 2), k + j * kRows * (D / 2), n);
-                copy16(dst + ln.dv + (16 * q + j * kRows) * (D / 2), w + j * kRows * (D / 2), n);
-            }
-        }
-        if (ln.scales) {
-            const int n = (ln.skey < 16 ? ok[0] : ok[1]) ? min(16, max(0, sp.hi - k0 - ln.skey) * (D / 16)) : 0;
-            copy16(dst + ln.ds, ln.s + (uint64_t)(ln.skey < 16 ? row[0] : row[1]) * (D / 16), n);
+        for (int j = 0; j < 16 / kRows; j++) {
+            const int n = ok[q] && k0 + 16 * q + j * kRows + ln.key < sp.hi ? 16 : 0;
+            copy16(dst + ln.dk + (16 * q + j * kRows) * (D / 2), k + j * kRows * (D / 2), n);
+            copy16(dst + ln.dv + (16 * q + j * kRows) * (D / 2), w + j * kRows * (D / 2), n);
         }
     }
+    if (ln.scales) {
+        const int n = (ln.skey < 16 ? ok[0] : ok[1]) ? min(16, max(0, sp.hi - k0 - ln.skey) * (D / 16)) : 0;
+        copy16(dst + ln.ds, ln.s + (uint64_t)(ln.skey < 16 ? row[0] : row[1]) * (D / 16), n);
+    }
+}
+
+// The same for a tile of 32 keys that all count and lie in one page of the
+// cache, from cache row `row` on.
+template <int D>
+__device__ __forceinline__ void load_whole_tile(const CopyLane<D>& ln, uint32_t row, uint32_t dst) {
+    constexpr int kRows = CopyLane<D>::kRows;
+    const uint8_t *k = ln.k + (uint64_t)row * (D / 2), *w = ln.v + (uint64_t)row * (D / 2);
+#pragma unroll
+    for (int j = 0; j < kKeys / kRows; j++) {
+        copy16(dst + ln.dk + j * kRows * (D / 2), k + j * kRows * (D / 2), 16);
+        copy16(dst + ln.dv + j * kRows * (D / 2), w + j * kRows * (D / 2), 16);
+    }
+    if (ln.scales) copy16(dst + ln.ds, ln.s + (uint64_t)(row + (ln.skey & kGroup)) * (D / 16), 16);
 }
 
 template <int N>
@@ -378,30 +379,47 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
     const CopyLane<D> ln(v, lane);
     const int32_t* table = v.pages + (int64_t)b * v.max_pages;
 
-    // copies run kStages - 1 tiles ahead, page lookups one more
-    int pages[2];
-    auto lookup = [&](int i) {
-        if (i < end) {
-            const int k0 = tiles.key0(i);
-            pages[0] = group_page(v, table, rows.span, k0);
-            // (a page of 2^5 or more tokens holds both groups of a tile)
-            pages[1] = v.page_shift >= 5 && pages[0] >= 0 && group_seen(rows.span, k0 + 16)
-                           ? pages[0]
-                           : group_page(v, table, rows.span, k0 + 16);
+    // Copies run kStages - 1 tiles ahead, page lookups one more.  A tile whose 32 keys are all seen by some row and
+    // lie in one page (of 32 or more tokens) takes the short way.
+    const Span& sp = rows.span;
+    const int jump = tiles.first > tiles.n_sink ? tiles.n_sink * kKeys : -1, after_jump = tiles.first * kKeys;
+    auto step = [&](int k0) { return k0 + kKeys == jump ? after_jump : k0 + kKeys; };  // from the sinks' tiles to the others
+    auto whole = [&](int k0) {
+        return v.page_shift >= 5 && ((k0 >= sp.lo && k0 + kKeys <= sp.hi) || k0 + kKeys <= sp.sink_end);
+    };
+    int page0 = -1, page1 = -1;
+    auto lookup = [&](int k0) {
+        if (whole(k0)) {
+            const int i = k0 >> v.page_shift;
+            page0 = page1 = i < v.max_pages ? __ldg(table + i) : -2;
+        } else {
+            page0 = group_page(v, table, sp, k0);
+            page1 = group_page(v, table, sp, k0 + kGroup);
         }
     };
-    auto fetch = [&](int i, int slot) {
-        if (i < end)
-            load_tile<D>(v, ln, b, page_rows, head_row, rows.span, tiles.key0(i), pages,
-                         ring + (uint32_t)(slot * Ring<D>::bytes));
+    auto fetch = [&](int k0, uint32_t dst) {
+        if (whole(k0) && (unsigned)page0 < (unsigned)v.n_pages) {
+            load_whole_tile<D>(ln, (uint32_t)page0 * page_rows + head_row + (uint32_t)(k0 & (v.page_size - 1)), dst);
+        } else {
+            const int pages[2] = {page0, page1};
+            load_tile<D>(v, ln, b, page_rows, head_row, sp, k0, pages, dst);
+        }
+    };
+    const uint32_t ring_end = ring + Ring<D>::kStages * Ring<D>::bytes;
+    int ahead = begin, ahead_k0 = tiles.key0(begin);  // the next tile to fetch, its page already looked up
+    uint32_t dst = ring;
+    if (ahead < end) lookup(ahead_k0);
+    auto advance = [&]() {
+        if (ahead < end) {
+            fetch(ahead_k0, dst);
+            dst = dst + Ring<D>::bytes == ring_end ? ring : dst + Ring<D>::bytes;
+            ahead_k0 = step(ahead_k0);
+            if (++ahead < end) lookup(ahead_k0);
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    lookup(begin);
-#pragma unroll
-    for (int i = 0; i < Ring<D>::kStages - 1; i++) {
-        fetch(begin + i, i);
-        lookup(begin + i + 1);
-    }
+#pragma unroll 1
+    for (int i = 0; i < Ring<D>::kStages - 1; i++) advance();
 
     // queries: column n of tile j is row f0 + 8 j + n; columns past the last row are zeros and nobody reads them
     uint32_t qb[NT][D / 8];
@@ -419,8 +437,10 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
 #pragma unroll
         for (int e = 0; e < 2; e++) c_col[j][e] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4 * e);
     }
-    const int p_first = s.len - s.n + f0 / a.group;  // the unit's first and last positions
-    const int p_last = s.len - s.n + (f0 + rows.n - 1) / a.group;
+    // a tile from k0 on is seen whole by every row when k0 <= all_hi and k0 >= all_lo or <= all_sink
+    const int all_hi = s.len - s.n + f0 / a.group - (kKeys - 1);
+    const int all_lo = a.window > 0 ? s.len - s.n + (f0 + rows.n - 1) / a.group - a.window + 1 : 0;
+    const int all_sink = a.sinks - kKeys;
 
     // a column's reference maximum m as -m, and what an exponent relative to it must exceed for m to move; before
     // its first visible key m is 0 and any exponent does
@@ -445,17 +465,14 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
     const uint32_t l_v0 = Ring<D>::v + v0 * (D / 2) + (D == 128 ? 16 * ((g >> 1) ^ (v0 & 2)) + 8 * (g & 1) : 4 * g);
     const uint32_t l_v1 = Ring<D>::v + v1 * (D / 2) + (D == 128 ? 16 * ((g >> 1) ^ (v1 & 2)) + 8 * (g & 1) : 4 * g);
     const uint32_t l_vs = Ring<D>::vs + (D == 128 ? g : g / 2);
-    int slot = 0;
+    int k0 = tiles.key0(begin);
+    uint32_t at = ring;
 
 #pragma unroll 1
-    for (int i = begin; i < end; i++) {
-        const int k0 = tiles.key0(i);
+    for (int i = begin; i < end; i++, k0 = step(k0), at = at + Ring<D>::bytes == ring_end ? ring : at + Ring<D>::bytes) {
         asm volatile("cp.async.wait_group %0;" ::"n"(Ring<D>::kStages - 2) : "memory");
         __syncwarp();  // the tile is there for every lane, and every lane has left the slot that is filled next
-        fetch(i + Ring<D>::kStages - 1, (slot + Ring<D>::kStages - 1) % Ring<D>::kStages);
-        lookup(i + Ring<D>::kStages);
-        const uint32_t at = ring + (uint32_t)(slot * Ring<D>::bytes);
-        slot = (slot + 1) % Ring<D>::kStages;
+        advance();
         // z: the scores' exponents, relative to the reference: 2^z is the weight
         float z[2][NT][4];
 #pragma unroll
@@ -468,10 +485,9 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
             decode_k<D>(w, D == 128 ? lds_u16(s16 + 8 * (D / 16)) : lds_u8(s16 + 8 * (D / 16)) * 0x101u, kb);
 #pragma unroll
             for (int j = 0; j < NT; j++) {
+                mma_16816_first(z[q][j], ka[0], kb[0], ka[1], kb[1], qb[j][0], qb[j][1]);
 #pragma unroll
-                for (int e = 0; e < 4; e++) z[q][j][e] = 0.0f;
-#pragma unroll
-                for (int e = 0; e < kSteps; e++)
+                for (int e = 1; e < kSteps; e++)
                     mma_16816(z[q][j], ka[2 * e], kb[2 * e], ka[2 * e + 1], kb[2 * e + 1], qb[j][2 * e], qb[j][2 * e + 1]);
             }
         }
@@ -482,9 +498,7 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
 #pragma unroll
                 for (int e = 0; e < 4; e++) z[q][j][e] = fmaf(z[q][j][e], c_col[j][e & 1], nm[j][e & 1]);
         // every key of the tile seen by every row, or else key by key
-        const bool all = k0 + kKeys - 1 <= p_first &&
-                         (a.window == 0 || k0 > p_last - a.window || k0 + kKeys <= a.sinks);
-        if (!all) {
+        if (!(k0 <= all_hi && (k0 >= all_lo || k0 <= all_sink))) {
 #pragma unroll
             for (int j = 0; j < NT; j++)
 #pragma unroll
@@ -643,20 +657,30 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     float mx = kFloor, sum = 0.0f, y[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; e++) y[e] = 0.0f;
-    for (int p = lane; p < cut.x; p += 32) mx = fmaxf(mx, __ldcg(&a.part_ml[at(p)].x));
+    for (int p0 = 0; p0 < cut.x; p0 += 32) {
+        // a lane has the weight of one piece
+        const int count = min(32, cut.x - p0);
+        const float2 ml = lane < count ? __ldcg(a.part_ml + at(p0 + lane)) : make_float2(kFloor, 0.0f);
+        float top = fmaxf(mx, ml.x);
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-#pragma unroll 4
-    for (int p = 0; p < cut.x; p++) {
-        const int64_t k = at(p);
-        const float2 ml = __ldcg(a.part_ml + k);
-        const float w = ex2(ml.x - mx);
-        sum += ml.y * w;
+        for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        const float before = ex2(mx - top), w = lane < count ? ex2(ml.x - top) : 0.0f;
+        mx = top;
+        float add = ml.y * w;
 #pragma unroll
-        for (int e = 0; e < D / 64; e++) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(a.part_o + k * D) + 32 * e + lane);
-            y[2 * e] += x.x * w;
-            y[2 * e + 1] += x.y * w;
+        for (int d = 1; d < 32; d *= 2) add += __shfl_xor_sync(0xFFFFFFFFu, add, d);
+        sum = sum * before + add;
+#pragma unroll
+        for (int e = 0; e < D / 32; e++) y[e] *= before;
+#pragma unroll 8
+        for (int p = 0; p < count; p++) {
+            const float wp = __shfl_sync(0xFFFFFFFFu, w, p);
+#pragma unroll
+            for (int e = 0; e < D / 64; e++) {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(a.part_o + at(p0 + p) * D) + 32 * e + lane);
+                y[2 * e] += x.x * wp;
+                y[2 * e + 1] += x.y * wp;
+            }
         }
     }
     const float f2 = sum > 0.0f ? __fdiv_rn(__ldg(v.a32[1]), sum) : 0.0f;
