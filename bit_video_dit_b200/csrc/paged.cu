@@ -237,7 +237,6 @@ __device__ __forceinline__ int group_page(const View& v, const int32_t* table, c
 // the reads below over all banks.
 template <int D>
 struct Ring {
-    static constexpr int kStages = 4;
     static constexpr int kCodes = kKeys * D / 2, kScales = kKeys * D / 16;
     static constexpr int k = 0, v = kCodes, ks = 2 * kCodes, vs = 2 * kCodes + kScales;
     static constexpr int bytes = 2 * (kCodes + kScales);
@@ -353,19 +352,11 @@ __device__ __forceinline__ void decode_k(const uint32_t* c, uint32_t sc, uint32_
     for (int w = 0; w < D / 32; w++) decode8(c[w], w < D / 64 ? s0 : s1, o + 4 * w);
 }
 
-template <int D>
-constexpr int decode_smem() {
-    return kWarps * Ring<D>::kStages * Ring<D>::bytes;
-}
-
-// CTAs of a launch: three an SM (two with 16 columns) by registers and shared memory.
-template <int NT>
-constexpr int decode_ctas() {
-    return kSms * (NT == 1 ? 3 : 2);
-}
-
-template <int D, int NT>
-__device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, uint32_t ring) {
+// One warp, one piece: kStages tiles in its ring at `ring`.  A piece that is not
+// the whole unit goes to slot u.slot of part_o and part_ml.
+template <int D, int NT, int kStages>
+__device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, uint32_t ring, float* part_o,
+                                             float2* part_ml) {
     constexpr int kCols = 8 * NT, kSteps = D / 16, kPer = D / 8;  // kPer: a lane's channels of O
     const View& v = a.v;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -405,7 +396,7 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
             load_tile<D>(v, ln, b, page_rows, head_row, sp, k0, pages, dst);
         }
     };
-    const uint32_t ring_end = ring + Ring<D>::kStages * Ring<D>::bytes;
+    const uint32_t ring_end = ring + kStages * Ring<D>::bytes;
     int ahead = begin, ahead_k0 = tiles.key0(begin);  // the next tile to fetch, its page already looked up
     uint32_t dst = ring;
     if (ahead < end) lookup(ahead_k0);
@@ -419,7 +410,7 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll 1
-    for (int i = 0; i < Ring<D>::kStages - 1; i++) advance();
+    for (int i = 0; i < kStages - 1; i++) advance();
 
     // queries: column n of tile j is row f0 + 8 j + n; columns past the last row are zeros and nobody reads them
     uint32_t qb[NT][D / 8];
@@ -470,7 +461,7 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
 
 #pragma unroll 1
     for (int i = begin; i < end; i++, k0 = step(k0), at = at + Ring<D>::bytes == ring_end ? ring : at + Ring<D>::bytes) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(Ring<D>::kStages - 2) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
         __syncwarp();  // the tile is there for every lane, and every lane has left the slot that is filled next
         advance();
         // z: the scores' exponents, relative to the reference: 2^z is the weight
@@ -598,11 +589,11 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
             if (n >= rows.n) continue;
             if (u.slot >= 0) {
                 const int64_t at = (int64_t)u.slot * kCols + n;
-                float4* dst = reinterpret_cast<float4*>(a.part_o + at * D + kPer * g);
+                float4* dst = reinterpret_cast<float4*>(part_o + at * D + kPer * g);
 #pragma unroll
                 for (int r = 0; r < kSteps; r += 2)
                     dst[r / 2] = make_float4(o[j][r][e], o[j][r][e + 2], o[j][r + 1][e], o[j][r + 1][e + 2]);
-                if (g == 0) a.part_ml[at] = make_float2(limit[j][e] == kLazy ? -nm[j][e] : kFloor, sum);
+                if (g == 0) part_ml[at] = make_float2(limit[j][e] == kLazy ? -nm[j][e] : kFloor, sum);
             } else {
                 const float f = sum > 0.0f ? __fdiv_rn(back, sum) : 0.0f;  // a row that sees no key: zeros
                 const int row = s.first + (f0 + n) / a.group, qh = head * a.group + (f0 + n) % a.group;
@@ -621,6 +612,18 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
         }
 }
 
+// CTAs of a launch: three an SM (two with 16 columns) by registers and shared memory.
+template <int NT>
+constexpr int decode_ctas() {
+    return kSms * (NT == 1 ? 3 : 2);
+}
+constexpr int kDecodeStages = 4;
+constexpr int kLeast = 8;  // tiles of a run: with fewer, joining many pieces takes longer (one sequence of 6000 keys: 36 us with 1, 21 with 8)
+template <int D>
+constexpr int decode_smem() {
+    return kWarps * kDecodeStages * Ring<D>::bytes;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(128) uint8_t ring_mem[];
@@ -628,16 +631,76 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(co
     asm volatile("griddepcontrol.wait;" ::: "memory");
     RunScratch<kWarps * 32>& scratch = *reinterpret_cast<RunScratch<kWarps * 32>*>(ring_mem);
     const int warp = threadIdx.x >> 5;
-    const uint32_t ring = smem_u32(ring_mem) + (uint32_t)(warp * Ring<D>::kStages * Ring<D>::bytes);
-    Run run = make_run<8 * NT, kKeys, kWarps * 32, kWarps>(a, warp, 1, scratch);
+    const uint32_t ring = smem_u32(ring_mem) + (uint32_t)(warp * kDecodeStages * Ring<D>::bytes);
+    Run run = make_run<8 * NT, kKeys, kWarps * 32, kWarps>(a, warp, kLeast, scratch);
     __syncthreads();  // the rings take the scratch memory over
     Piece u;
     int4 cut = make_int4(0, 0, 0, 0);
     while (next_piece<8 * NT, kKeys>(a, run, u)) {
-        decode_piece<D, NT>(a, u, ring);
+        decode_piece<D, NT, kDecodeStages>(a, u, ring, a.part_o, a.part_ml);
         if (u.pieces) cut = make_int4(u.pieces, u.pair, u.head, 0);
     }
     if ((threadIdx.x & 31) == 0) a.cut[run.worker] = cut;
+}
+
+// Short sequences: a unit a CTA, its tiles shared out among eight warps that
+// join in shared memory, so that one launch does.  Up to 64 tiles (2048 keys)
+// it is the faster way (1, 8 and 64 sequences of 8 heads of 128: 700 keys 9.1,
+// 9.1, 10.4 us against 13.7, 16.8, 14.5 with runs; 1500 keys 11.3, 14.9, 32.8
+// against 19.4, 18.2, 35.2; 3000 keys 18.6, 26.2, 54.8 against 18.4, 20.8,
+// 55.7), and sequences much shorter than the longest cost it little.
+constexpr int kUnitWarps = 8, kUnitStages = 2;
+constexpr int kUnitTiles = 64;  // the longest sequence (tiles) that takes this way
+template <int D>
+constexpr int unit_smem() {
+    // (a warp leaves its piece, up to 16 columns, where its ring was)
+    static_assert(16 * (D * 4 + 8) <= kUnitStages * Ring<D>::bytes, "piece");
+    return kUnitWarps * kUnitStages * Ring<D>::bytes;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kUnitWarps * 32, NT == 1 ? 2 : 1) unit_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int kCols = 8 * NT, kBytes = kUnitStages * Ring<D>::bytes;
+    extern __shared__ __align__(128) uint8_t ring_mem[];
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const View& v = a.v;
+    const int warp = threadIdx.x >> 5;
+    Piece u;
+    int real = 0;
+    const int pair = (int)(blockIdx.x / (unsigned)v.kv_heads);
+    u.head = (int)(blockIdx.x % (unsigned)v.kv_heads);
+    if (pair_tiles<kCols, kKeys>(a, pair, &u.s, &u.rows, &real) == 0) return;
+    u.b = pair / a.row_tiles;
+    u.f0 = pair % a.row_tiles * kCols;
+    u.begin = real * warp / kUnitWarps;
+    u.end = real * (warp + 1) / kUnitWarps;
+    u.slot = 0;
+    float* part = reinterpret_cast<float*>(ring_mem + warp * kBytes);
+    decode_piece<D, NT, kUnitStages>(a, u, smem_u32(ring_mem) + (uint32_t)(warp * kBytes), part,
+                                     reinterpret_cast<float2*>(part + kCols * D));
+    __syncthreads();
+    const float back = __ldg(v.a32[1]);
+    for (int i = threadIdx.x; i < u.rows.n * (D / 2); i += kUnitWarps * 32) {
+        const int n = i / (D / 2), d = i % (D / 2) * 2;
+        float mx = kFloor, sum = 0.0f, y0 = 0.0f, y1 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kUnitWarps; w++)
+            mx = fmaxf(mx, reinterpret_cast<const float2*>(ring_mem + w * kBytes + kCols * D * 4)[n].x);
+#pragma unroll
+        for (int w = 0; w < kUnitWarps; w++) {
+            const float2 ml = reinterpret_cast<const float2*>(ring_mem + w * kBytes + kCols * D * 4)[n];
+            const float2 x = *reinterpret_cast<const float2*>(ring_mem + w * kBytes + (n * D + d) * 4);
+            const float f = ex2(ml.x - mx);
+            sum += ml.y * f;
+            y0 += x.x * f;
+            y1 += x.y * f;
+        }
+        const int row = u.s.first + (u.f0 + n) / a.group, qh = u.head * a.group + (u.f0 + n) % a.group;
+        const float f = sum > 0.0f ? __fdiv_rn(back, sum) : 0.0f;  // a row that sees no key: zeros
+        *reinterpret_cast<__nv_bfloat162*>(a.o + ((int64_t)row * a.ld_o + (int64_t)qh * D + d) * 2) =
+            __floats2bfloat162_rn(y0 * f, y1 * f);
+    }
 }
 
 // Joins the pieces of the unit that worker blockIdx.x began, a warp a row.
@@ -806,6 +869,7 @@ nvfp4_status rows_call(bool append, const nvfp4_paged_cache* c, const nvfp4_page
 // How an attention call is launched; the same for its workspace query.
 struct Plan {
     bool chunks;  // chunk_kernel (paged_attention.cu), else decode_kernel
+    bool units;   // unit_kernel: no pieces
     int cols;     // (row, query head) pairs of a unit
     int row_tiles, ctas, workers;
     size_t cut, ml, o, ws;  // bytes from the workspace's start
@@ -823,12 +887,18 @@ bool make_plan(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, int heads,
     // no more CTAs than the shortest runs of the most tiles
     int64_t seen = r->max_len;
     if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + sinks + std::min<int64_t>(r->max_rows, p->cols));
-    const int keys = p->chunks ? kChunkKeys : kKeys, least = p->chunks ? kChunkLeast : kWarps;
+    const int keys = p->chunks ? kChunkKeys : kKeys, least = p->chunks ? kChunkLeast : kWarps * kLeast;
     p->workers = p->chunks ? 1 : kWarps;  // of a CTA
     const int64_t tiles = (seen / keys + 3) * p->row_tiles * std::max(1, r->n_seqs);  // ragged at both ends and the sinks'
     p->ctas = (int)std::min<int64_t>(p->ctas, (tiles * c->kv_heads + least - 1) / least);
+    const int64_t units = (int64_t)p->row_tiles * std::max(1, r->n_seqs) * c->kv_heads;
+    p->units = !p->chunks && seen / keys < kUnitTiles && units < ((int64_t)1 << 31);
+    if (p->units) {
+        p->ctas = (int)units;
+        p->workers = 0;
+    }
     p->cut = kControl;
-    p->workers *= p->ctas;
+    p->workers *= p->units ? 0 : p->ctas;
     p->ml = p->cut + (size_t)p->workers * sizeof(int4);
     p->o = p->ml + (size_t)p->workers * 2 * p->cols * sizeof(float2);
     p->ws = p->o + (size_t)p->workers * 2 * p->cols * c->head_dim * sizeof(float);
@@ -904,26 +974,31 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, co
         st = launch_chunks(a, (unsigned)p.ctas, (cudaStream_t)stream);
         if (st != NVFP4_OK) return st;
     } else {
-        void (*kern)(AttnArgs) = cache->head_dim == 128 ? (p.cols == 8 ? decode_kernel<128, 1> : decode_kernel<128, 2>)
-                                                        : (p.cols == 8 ? decode_kernel<64, 1> : decode_kernel<64, 2>);
         static PerDevice<int> ready;
         int done = 0;
         st = ready.get(&done, [](int, int& v) {
             v = 1;
-            return cudaFuncSetAttribute(decode_kernel<128, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        decode_smem<128>()) == cudaSuccess &&
-                           cudaFuncSetAttribute(decode_kernel<128, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                decode_smem<128>()) == cudaSuccess &&
-                           cudaFuncSetAttribute(decode_kernel<64, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                decode_smem<64>()) == cudaSuccess &&
-                           cudaFuncSetAttribute(decode_kernel<64, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                decode_smem<64>()) == cudaSuccess
+            auto room = [](void (*f)(AttnArgs), int bytes) {
+                return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+            };
+            return room(decode_kernel<128, 1>, decode_smem<128>()) && room(decode_kernel<128, 2>, decode_smem<128>()) &&
+                           room(decode_kernel<64, 1>, decode_smem<64>()) && room(decode_kernel<64, 2>, decode_smem<64>()) &&
+                           room(unit_kernel<128, 1>, unit_smem<128>()) && room(unit_kernel<128, 2>, unit_smem<128>()) &&
+                           room(unit_kernel<64, 1>, unit_smem<64>()) && room(unit_kernel<64, 2>, unit_smem<64>())
                        ? NVFP4_OK
                        : NVFP4_ERR_CUDA;
         });
         if (st != NVFP4_OK) return st;
-        st = launch_dependent(kern, dim3((unsigned)p.ctas), kWarps * 32,
-                              cache->head_dim == 128 ? decode_smem<128>() : decode_smem<64>(), (cudaStream_t)stream, a);
+        const bool wide = cache->head_dim == 128, one = p.cols == 8;
+        if (p.units)
+            return launch_dependent(wide ? (one ? unit_kernel<128, 1> : unit_kernel<128, 2>)
+                                         : (one ? unit_kernel<64, 1> : unit_kernel<64, 2>),
+                                    dim3((unsigned)p.ctas), kUnitWarps * 32, wide ? unit_smem<128>() : unit_smem<64>(),
+                                    (cudaStream_t)stream, a);
+        st = launch_dependent(wide ? (one ? decode_kernel<128, 1> : decode_kernel<128, 2>)
+                                   : (one ? decode_kernel<64, 1> : decode_kernel<64, 2>),
+                              dim3((unsigned)p.ctas), kWarps * 32, wide ? decode_smem<128>() : decode_smem<64>(),
+                              (cudaStream_t)stream, a);
         if (st != NVFP4_OK) return st;
     }
     void (*join)(AttnArgs) =

@@ -474,8 +474,9 @@ nvfp4_status nvfp4_paged_gather(const nvfp4_paged_cache* cache, const nvfp4_page
  * (max_rows * heads / kv_heads) run on a kernel for decode steps, more on one
  * for chunks (tcgen05), whose waits are bounded: one that runs out records
  * NVFP4_ERR_TIMEOUT (info = which wait) and leaves o incomplete.  Both deal the
- * key tiles out to the CTAs in equal runs, whatever the lengths; a second launch
- * joins the rows whose keys lie in several runs. */
+ * key tiles out in equal runs, whatever the lengths, and a second launch joins
+ * the rows whose keys lie in several runs; decode steps whose spans (max_len, or
+ * window and sinks) are below 2048 keys take one launch. */
 size_t nvfp4_paged_attention_workspace_bytes(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows,
                                              int32_t heads, int32_t window, int32_t sinks);
 nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows, const void* q_bf16,

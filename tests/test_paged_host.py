@@ -113,10 +113,10 @@ def test_attention_workspace_query(L):
         return L.nvfp4_paged_attention_workspace_bytes(ctypes.byref(_cache(**c)), ctypes.byref(_rows(**r)), heads, window,
                                                        sinks)
 
-    assert need() > 256
     # two pieces of a unit a CTA: no more for more sequences once every SM has its CTAs; larger for chunks
     assert need(max_len=100000) == need(max_len=200000) == need(n_seqs=700, n_rows=1000, max_len=100000) > need()
-    assert need(max_len=100000) == need(max_len=100000, window=100, n_seqs=1000) > need(max_len=100000, window=100)
+    assert need() == need(max_len=100000, window=100) == 256  # short spans are not cut into pieces
+    assert need(max_len=100000) == need(max_len=100000, window=9000, n_seqs=1000)
     long = need(max_rows=100, max_len=100000)
     assert need(max_len=100000) < need(max_rows=8, max_len=100000) < long <= 40 << 20
     assert need(heads=3) == 0 and need(window=-1) == 0 and need(c=dict(head_dim=80)) == 0
