@@ -187,30 +187,38 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) gemv_kernel(const __grid
 
     float down[NT][2];  // what the sums' columns 2t, 2t + 1 are multiplied by
     if (XS) {
-        // the rows' largest magnitudes, then the scaled rows
+        // the rows' largest magnitudes, then the scaled rows; a thread keeps what it has read (a warp has whole rows'
+        // parts, of 32 x 8 activations, so that its maximum is one row's)
+        constexpr int kParts = (Cfg<NT>::kX / 16 + kThreads - 1) / kThreads + 1;
+        const int row_parts = (a.chunks * 16 + 31) / 32, parts = row_parts * a.m;
+        uint4 v[kParts];
         __syncthreads();
-        for (int m = 0; m < a.m; m++) {
-            const uint4* row = reinterpret_cast<const uint4*>(a.x + (int64_t)m * a.ldx * 2);
-            uint32_t mx = 0u;
-            for (int i = threadIdx.x; i < a.k / 8; i += kThreads) {
-                const uint4 v = __ldg(row + i);
-                mx = max(mx, max_bits<1>(&v));
-            }
-            mx = __reduce_max_sync(0xFFFFFFFFu, mx);
-            if (lane == 0) atomicMax(&row_max[m], mx);
+#pragma unroll
+        for (int i = 0; i < kParts; i++) {
+            const int p = warp + i * kWarps, m = p / row_parts, j = (p - m * row_parts) * 32 + lane;
+            v[i] = p < parts && j < a.k / 8 ? __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)m * a.ldx * 2) + j)
+                                            : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < kParts; i++) {
+            const int p = warp + i * kWarps;
+            if (p >= parts) break;
+            const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, max_bits<1>(&v[i]));
+            if (lane == 0) atomicMax(&row_max[p / row_parts], mx);
         }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < NT; j++)
 #pragma unroll
             for (int e = 0; e < 2; e++) down[j][e] = row_scale(row_max[8 * j + 2 * t + e]).down;
-        for (int m = 0; m < a.m; m++) {
-            const uint4* row = reinterpret_cast<const uint4*>(a.x + (int64_t)m * a.ldx * 2);
-            const float u = row_scale(row_max[m]).up;
-            for (int i = threadIdx.x; i < a.chunks * 16; i += kThreads) {
+#pragma unroll
+        for (int i = 0; i < kParts; i++) {
+            const int p = warp + i * kWarps, m = p / row_parts, j = (p - m * row_parts) * 32 + lane;
+            if (p >= parts) break;
+            if (j < a.chunks * 16) {
                 uint32_t h[4];
-                scale8(i < a.k / 8 ? __ldg(row + i) : make_uint4(0u, 0u, 0u, 0u), u, h);
-                st_shared16(xs + ((i >> 4) * a.m + m) * 256 + x_place(m, i & 15) * 16, make_uint4(h[0], h[1], h[2], h[3]));
+                scale8(v[i], row_scale(row_max[m]).up, h);
+                st_shared16(xs + ((j >> 4) * a.m + m) * 256 + x_place(m, j & 15) * 16, make_uint4(h[0], h[1], h[2], h[3]));
             }
         }
         __syncthreads();
@@ -391,7 +399,7 @@ extern "C" nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t m, int64_t ldx, c
     cfg.gridDim = dim3((unsigned)(a.groups < gemv::kSms ? a.groups : gemv::kSms));
     const bool two = m > 8;
     const int64_t xbytes = (int64_t)a.chunks * m * 256, room = two ? gemv::Cfg<2>::kX : gemv::Cfg<1>::kX;
-    const bool xs = xbytes <= room;
+    const bool xs = xbytes <= room;  // (then at most 100 or 33 parts, of the 128 or 48 that the warps hold)
     cfg.blockDim = dim3((unsigned)(two ? gemv::Cfg<2>::kThreads : gemv::Cfg<1>::kThreads));
     cfg.dynamicSmemBytes = (size_t)((two ? gemv::Cfg<2>::kRing + gemv::Cfg<2>::kPart
                                          : gemv::Cfg<1>::kRing + gemv::Cfg<1>::kPart) + (xs ? xbytes : 0));

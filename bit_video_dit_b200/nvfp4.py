@@ -359,12 +359,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _launch_on(device: torch.device, stream, fn, *args) -> int:
-    """Call fn(*args, stream) with `device` current (its current stream when none is given)."""
-    raw = _raw_stream(device.index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+def _launch_on(index: int, stream, fn, *args) -> int:
+    """Call fn(*args, stream) with device `index` current (its current stream when none is given)."""
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
         return fn(*args, raw)
-    with torch.cuda.device(device):
+    with torch.cuda.device(index):
         return fn(*args, raw)
 
 
@@ -381,32 +381,43 @@ def gemv(x: torch.Tensor, w: NVFP4Tensor, *, out: torch.Tensor | None = None, ou
     """y[M, N] = x W^T with the NVFP4 weight w [N, K] (as gemm's b) and 1..16 rows x [M, K] of bf16 that are not
     quantized, then gemm's epilogue (bias, act, modulate, gate, residual); bf16 `out` [M, N] (rows may be strided)
     and, when out_f32 is given, the same in float32 before the store."""
-    _require_cuda(x)
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != w.cols or x.stride(1) != 1:
-        raise ValueError("gemv takes bf16 x [M, K] with unit column stride and K of the weight")
-    M, N = x.shape[0], w.rows
-    device = x.device
+    # (the checks are written for few calls into torch: a small product takes no longer than they do)
+    index, N = x.get_device(), w.rows
+    if index < 0:
+        raise ValueError("libnvfp4 works on CUDA tensors only")
+    if x.dim() != 2 or x.dtype != torch.bfloat16:
+        raise ValueError("gemv takes 2-D bf16 x")
+    (M, K), (ldx, sx) = x.shape, x.stride()
+    if K != w.cols or sx != 1:
+        raise ValueError("gemv takes x [M, K] with unit column stride and K of the weight")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=device)
-    elif out.dtype != torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1:
-        raise ValueError("out is bf16 [M, N] with unit column stride")
-    _same_device(device, w.codes, out, out_f32, bias, mod_scale, mod_shift, gate, residual)
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    elif out.dtype != torch.bfloat16 or out.shape != (M, N):
+        raise ValueError("out is bf16 [M, N]")
+    ldy, sy = out.stride()
+    if (sy != 1 and N > 1) or out.get_device() != index or w.codes.get_device() != index:
+        raise ValueError(f"x, the weight and out have to be on {x.device}, out with unit column stride")
     ep = None
     if act or not (bias is mod_scale is mod_shift is gate is residual is out_f32 is None):
-        for v in (bias, mod_scale, mod_shift, gate):
-            if v is not None and (v.dtype != torch.bfloat16 or v.numel() != N or not v.is_contiguous()):
-                raise ValueError("bias, mod_scale, mod_shift and gate are contiguous bf16 [N]")
-        if residual is not None and (residual.dtype != torch.bfloat16 or residual.shape != (M, N) or
-                                     residual.stride(1) != 1):
-            raise ValueError("residual is bf16 [M, N] with unit column stride")
-        if out_f32 is not None and (out_f32.dtype != torch.float32 or out_f32.shape != (M, N) or
-                                    not out_f32.is_contiguous()):
-            raise ValueError("out_f32 is contiguous float32 [M, N]")
-        ep = ctypes.byref(make_epilogue(bias=bias, mod_scale=mod_scale, mod_shift=mod_shift, gate=gate,
-                                        residual=residual, act=act, debug_y=out_f32))
-    # a row stride means nothing for a single row
-    ldx, ldy = (x.stride(0), out.stride(0)) if M > 1 else (w.cols, N)
-    st = _launch_on(device, stream, lib().nvfp4_gemv, x.data_ptr(), M, ldx, ctypes.byref(w.c()), out.data_ptr(), ldy, ep)
+        _same_device(x.device, out_f32, bias, mod_scale, mod_shift, gate, residual)
+        e = CEpilogue(act=act)
+        for name, v in (("bias", bias), ("mod_scale", mod_scale), ("mod_shift", mod_shift), ("gate", gate)):
+            if v is not None:
+                if v.dtype != torch.bfloat16 or v.numel() != N or not v.is_contiguous():
+                    raise ValueError("bias, mod_scale, mod_shift and gate are contiguous bf16 [N]")
+                setattr(e, name, v.data_ptr())
+        if residual is not None:
+            if residual.dtype != torch.bfloat16 or residual.shape != (M, N) or (residual.stride(1) != 1 and N > 1):
+                raise ValueError("residual is bf16 [M, N] with unit column stride")
+            e.residual, e.ld_residual = residual.data_ptr(), residual.stride(0) if M > 1 else N
+        if out_f32 is not None:
+            if out_f32.dtype != torch.float32 or out_f32.shape != (M, N) or not out_f32.is_contiguous():
+                raise ValueError("out_f32 is contiguous float32 [M, N]")
+            e.debug_y = out_f32.data_ptr()
+        ep = ctypes.byref(e)
+    if M <= 1:  # a row stride means nothing for a single row
+        ldx, ldy = K, N
+    st = _launch_on(index, stream, lib().nvfp4_gemv, x.data_ptr(), M, ldx, ctypes.byref(w.c()), out.data_ptr(), ldy, ep)
     if st:
         _check("nvfp4_gemv", st)
     return out
@@ -528,6 +539,7 @@ class PagedRows:
         _same_device(lens.device, row_start, pages)
         self.row_start, self.lens, self.pages = row_start, lens, pages
         self.n_seqs, self.n_rows, self.max_rows, self.max_len = B, n_rows, max_rows, max_len
+        self.index = lens.get_device()
         self._c = CPagedRows(row_start.data_ptr(), lens.data_ptr(), pages.data_ptr(), B, pages.shape[1], n_rows,
                              max_rows, max_len)
         self._ref = ctypes.byref(self._c)
@@ -550,7 +562,9 @@ class PagedKVCache:
         self.v_codes = torch.zeros((*shape, head_dim // 2), dtype=u8, device=device)
         self.k_scales = torch.zeros((*shape, head_dim // 16), dtype=u8, device=device)
         self.v_scales = torch.zeros((*shape, head_dim // 16), dtype=u8, device=device)
-        self.device = self.k_codes.device
+        self.device, self.index = self.k_codes.device, self.k_codes.get_device()
+        if self.index < 0:
+            raise ValueError("libnvfp4 works on CUDA tensors only")
         # (the cache keeps its own copies: a later change of the caller's tensors does not reach the pages written)
         self.k_global = torch.as_tensor(k_scale, dtype=torch.float32, device=self.device).reshape(1).clone()
         self.v_global = torch.as_tensor(v_scale, dtype=torch.float32, device=self.device).reshape(1).clone()
@@ -567,27 +581,23 @@ class PagedKVCache:
         return sum(t.numel() * t.element_size() for t in
                    (self.k_codes, self.v_codes, self.k_scales, self.v_scales, self.k_global, self.v_global))
 
-    def _row_strides(self, rows: PagedRows, heads: int, *ts) -> list[int]:
-        """Elements between the rows of [n_rows, heads, head_dim] tensors, which have to be fit for the call."""
-        index, d, shape, lds = self.device.index, self.head_dim, (rows.n_rows, heads, self.head_dim), []
-        if rows.lens.get_device() != index:
-            raise ValueError(f"the rows have to be on {self.device}")
-        for t in ts:
-            if t.get_device() != index:
-                raise ValueError(f"every tensor of the call has to be on {self.device}")
-            if t.dtype != torch.bfloat16 or t.shape != shape:
-                raise ValueError(f"row tensors are bf16 {list(shape)}: got {t.dtype} {list(t.shape)}")
-            ld, per_head, unit = t.stride()
-            if (unit != 1 or (per_head != d and heads > 1)) and rows.n_rows:
-                raise ValueError("the heads of a row have to be contiguous")
-            lds.append(ld if rows.n_rows > 1 else heads * d)  # a row stride means nothing for a single row
-        return lds
+    def _row_stride(self, rows: PagedRows, heads: int, t: torch.Tensor) -> int:
+        """Elements between the rows of a [n_rows, heads, head_dim] tensor, which has to be fit for the call."""
+        if t.get_device() != self.index or rows.index != self.index:
+            raise ValueError(f"the rows and every tensor of the call have to be on {self.device}")
+        if t.dtype != torch.bfloat16 or t.shape != (rows.n_rows, heads, self.head_dim):
+            raise ValueError(f"row tensors are bf16 {[rows.n_rows, heads, self.head_dim]}: got {t.dtype} {list(t.shape)}")
+        ld, per_head, unit = t.stride()
+        if (unit != 1 or (per_head != self.head_dim and heads > 1)) and rows.n_rows:
+            raise ValueError("the heads of a row have to be contiguous")
+        return ld if rows.n_rows > 1 else heads * self.head_dim  # a row stride means nothing for a single row
 
     def append(self, rows: PagedRows, k: torch.Tensor, v: torch.Tensor, *, rope=None, ws: torch.Tensor | None = None,
                stream=None) -> None:
         """Quantize the rows' K and V (bf16 [n_rows, kv_heads, d], rows may be strided) into their pages.  rope =
         (cos, sin), float32 [n_rows, d / 2] each: the keys are turned first (interleaved pairs, as KVCache.append)."""
-        ld_k, ld_v = self._row_strides(rows, self.kv_heads, k, v)
+        heads = self.kv_heads
+        ld_k, ld_v = self._row_stride(rows, heads, k), self._row_stride(rows, heads, v)
         cos = sin = None
         if rope is not None:
             cos, sin = rope
@@ -596,7 +606,7 @@ class PagedKVCache:
                     raise ValueError("rope tables are contiguous float32 [n_rows, d / 2]")
             _same_device(self.device, cos, sin)
         ws = self.ws_rows if ws is None else ws
-        st = _launch_on(self.device, stream, lib().nvfp4_paged_append, self._ref, rows._ref, k.data_ptr(), ld_k,
+        st = _launch_on(self.index, stream, lib().nvfp4_paged_append, self._ref, rows._ref, k.data_ptr(), ld_k,
                         v.data_ptr(), ld_v, _ptr(cos), _ptr(sin), ws.data_ptr(), ws.numel())
         if st:
             _check("nvfp4_paged_append", st)
@@ -604,14 +614,14 @@ class PagedKVCache:
     def gather(self, rows: PagedRows, *, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
                ws: torch.Tensor | None = None, stream=None):
         """Read the rows' K and V back to bf16 [n_rows, kv_heads, d]."""
-        shape = (rows.n_rows, self.kv_heads, self.head_dim)
         if k_out is None:
-            k_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            k_out = torch.empty((rows.n_rows, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        ld_k, ld_v = self._row_strides(rows, self.kv_heads, k_out, v_out)
+            v_out = torch.empty_like(k_out, memory_format=torch.contiguous_format)
+        heads = self.kv_heads
+        ld_k, ld_v = self._row_stride(rows, heads, k_out), self._row_stride(rows, heads, v_out)
         ws = self.ws_rows if ws is None else ws
-        st = _launch_on(self.device, stream, lib().nvfp4_paged_gather, self._ref, rows._ref, k_out.data_ptr(), ld_k,
+        st = _launch_on(self.index, stream, lib().nvfp4_paged_gather, self._ref, rows._ref, k_out.data_ptr(), ld_k,
                         v_out.data_ptr(), ld_v, ws.data_ptr(), ws.numel())
         if st:
             _check("nvfp4_paged_gather", st)
@@ -635,10 +645,10 @@ class PagedKVCache:
         heads = q.shape[1]
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        ld_q, ld_o = self._row_strides(rows, heads, q, out)
+        ld_q, ld_o = self._row_stride(rows, heads, q), self._row_stride(rows, heads, out)
         if ws is None:
             ws = self.attention_workspace(rows, heads, window=window, sinks=sinks)
-        st = _launch_on(self.device, stream, lib().nvfp4_paged_attention, self._ref, rows._ref, q.data_ptr(), ld_q,
+        st = _launch_on(self.index, stream, lib().nvfp4_paged_attention, self._ref, rows._ref, q.data_ptr(), ld_q,
                         heads, window, sinks, scale, out.data_ptr(), ld_o, ws.data_ptr(), ws.numel())
         if st:
             _check("nvfp4_paged_attention", st)
