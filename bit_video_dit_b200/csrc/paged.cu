@@ -224,11 +224,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 // Page of the 16 keys from kq on: -1 when no row of the unit sees one of them
-// (not looked up), else what the table lists (-2 behind its end).
+// (not looked up), else what the table lists.
 __device__ __forceinline__ int group_page(const View& v, const int32_t* table, const Span& sp, int kq) {
     if (!group_seen(sp, kq)) return -1;
-    const int i = v.page_shift >= 0 ? kq >> v.page_shift : kq / v.page_size;
-    return i < v.max_pages ? __ldg(table + i) : -2;
+    return listed(table, v.page_shift >= 0 ? kq >> v.page_shift : kq / v.page_size);
 }
 
 // A warp's ring of 32-key tiles in shared memory, filled by asynchronous
@@ -343,6 +342,13 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t p) {
 // keys t, 4 + (t ^ 1), and 8 more, in four different bank quarters each time.
 __device__ __forceinline__ int key_of_row(int r) { return (r & 1) ? 4 + ((r >> 1) ^ 1) : r >> 1; }
 
+// A key's D / 16 scales
+template <int D>
+__device__ __forceinline__ void clear_scales(uint32_t p) {
+    if (D == 128) asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(p), "r"(0u) : "memory");
+    else asm volatile("st.shared.u32 [%0], %1;" ::"r"(p), "r"(0u) : "memory");
+}
+
 // One key's D / 4 codes and their scales -> D / 8 pairs
 template <int D>
 __device__ __forceinline__ void decode_k(const uint32_t* c, uint32_t sc, uint32_t* o) {
@@ -381,8 +387,7 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
     int page0 = -1, page1 = -1;
     auto lookup = [&](int k0) {
         if (whole(k0)) {
-            const int i = k0 >> v.page_shift;
-            page0 = page1 = i < v.max_pages ? __ldg(table + i) : -2;
+            page0 = page1 = listed(table, k0 >> v.page_shift);
         } else {
             page0 = group_page(v, table, sp, k0);
             page1 = group_page(v, table, sp, k0 + kGroup);
@@ -464,6 +469,11 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
         __syncwarp();  // the tile is there for every lane, and every lane has left the slot that is filled next
         advance();
+        // places that no row sees (outside the window) may hold anything: their weight is 0, and their values' scale has to be
+        if (max(k0, sp.sink_end) < min(k0 + kKeys, sp.lo)) {
+            if (k0 + lane >= sp.sink_end && k0 + lane < sp.lo) clear_scales<D>(at + Ring<D>::vs + lane * (D / 16));
+            __syncwarp();
+        }
         // z: the scores' exponents, relative to the reference: 2^z is the weight
         float z[2][NT][4];
 #pragma unroll
@@ -595,7 +605,7 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
                     dst[r / 2] = make_float4(o[j][r][e], o[j][r][e + 2], o[j][r + 1][e], o[j][r + 1][e + 2]);
                 if (g == 0) part_ml[at] = make_float2(limit[j][e] == kLazy ? -nm[j][e] : kFloor, sum);
             } else {
-                const float f = sum > 0.0f ? __fdiv_rn(back, sum) : 0.0f;  // a row that sees no key: zeros
+                const float f = sum == 0.0f ? 0.0f : __fdiv_rn(back, sum);  // a row that sees no key: zeros
                 const int row = s.first + (f0 + n) / a.group, qh = head * a.group + (f0 + n) % a.group;
                 uint4* dst = reinterpret_cast<uint4*>(a.o + ((int64_t)row * a.ld_o + (int64_t)qh * D + kPer * g) * 2);
 #pragma unroll
@@ -697,7 +707,7 @@ __global__ void __launch_bounds__(kUnitWarps * 32, NT == 1 ? 2 : 1) unit_kernel(
             y1 += x.y * f;
         }
         const int row = u.s.first + (u.f0 + n) / a.group, qh = u.head * a.group + (u.f0 + n) % a.group;
-        const float f = sum > 0.0f ? __fdiv_rn(back, sum) : 0.0f;  // a row that sees no key: zeros
+        const float f = sum == 0.0f ? 0.0f : __fdiv_rn(back, sum);  // a row that sees no key: zeros
         *reinterpret_cast<__nv_bfloat162*>(a.o + ((int64_t)row * a.ld_o + (int64_t)qh * D + d) * 2) =
             __floats2bfloat162_rn(y0 * f, y1 * f);
     }
@@ -746,7 +756,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
             }
         }
     }
-    const float f2 = sum > 0.0f ? __fdiv_rn(__ldg(v.a32[1]), sum) : 0.0f;
+    const float f2 = sum == 0.0f ? 0.0f : __fdiv_rn(__ldg(v.a32[1]), sum);
     const int64_t row = s.first + f / a.group, qh = cut.z * a.group + f % a.group;
     __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + (row * a.ld_o + qh * D) * 2);
 #pragma unroll
@@ -832,6 +842,7 @@ View make_view(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, void* ws) 
     v.n_seqs = r->n_seqs;
     v.max_pages = r->max_pages;
     v.n_rows = r->n_rows;
+    v.room = (int)std::min<int64_t>((int64_t)r->max_pages * c->page_size, 1 << 30);
     v.err = static_cast<DevError*>(ws);
     return v;
 }
@@ -958,7 +969,6 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, co
     a.o = static_cast<uint8_t*>(o_bf16);
     a.ld_q = ld_q;
     a.ld_o = ld_o;
-    a.heads = heads;
     a.group = heads / cache->kv_heads;
     a.window = window;
     a.sinks = window > 0 ? sinks : 0;

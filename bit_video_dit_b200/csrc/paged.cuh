@@ -20,6 +20,7 @@ struct View {
     int n_pages, page_size, kv_heads, d;
     int page_shift;  // page_size = 2^page_shift, or -1
     int n_seqs, max_pages, n_rows;
+    int room;  // positions that a page table has room for (at most 2^30)
     DevError* err;
 };
 
@@ -29,15 +30,16 @@ struct Seq {
     int first, n, len;
 };
 
-// Sequence b; one whose rows do not lie in the row tensors is reported
-// (info = b) and taken as having none.
+// Sequence b; one whose rows do not lie in the row tensors, or whose length not
+// in the page table, is reported (info = b) and taken as having none: whatever
+// the arrays hold, a launch's work is bounded and no position overflows.
 __device__ __forceinline__ Seq load_seq(const View& v, int b) {
     Seq s;
     const int r0 = __ldg(v.row_start + b), r1 = __ldg(v.row_start + b + 1);
     s.first = r0;
     s.n = r1 - r0;
     s.len = __ldg(v.lens + b);
-    if (r0 < 0 || r1 < r0 || r1 > v.n_rows || s.len < 0) {
+    if (r0 < 0 || r1 < r0 || r1 > v.n_rows || s.len < 0 || s.len > v.room) {
         record_error(v.err, NVFP4_ERR_DEVICE, (uint32_t)b);
         s.n = 0;
         s.len = 0;
@@ -45,19 +47,20 @@ __device__ __forceinline__ Seq load_seq(const View& v, int b) {
     return s;
 }
 
-// The page that holds position pos of sequence b, or -1 (reported, info = b)
-// when the table does not list one of the cache's pages for it.
+// The page that holds position pos < len of sequence b, or -1 (reported, info =
+// b) when the table does not list one of the cache's pages for it.
 __device__ __forceinline__ int page_of(const View& v, int b, int pos) {
-    const int i = pos / v.page_size;
-    const int p = i < v.max_pages ? __ldg(v.pages + (int64_t)b * v.max_pages + i) : -1;
+    const int p = __ldg(v.pages + (int64_t)b * v.max_pages + pos / v.page_size);
     if (p >= 0 && p < v.n_pages) return p;
     record_error(v.err, NVFP4_ERR_DEVICE, (uint32_t)b);
     return -1;
 }
 
-// Row index of (page, head, position) in the cache's [..][head_dim] rows.
-__device__ __forceinline__ int64_t cache_row(const View& v, int page, int head, int pos) {
-    return ((int64_t)page * v.kv_heads + head) * v.page_size + pos % v.page_size;
+// Entry i of a sequence's page table for the attention, in which -1 stands for
+// a page that is not needed: an entry below 0 becomes -2.
+__device__ __forceinline__ int listed(const int32_t* table, int i) {
+    const int p = __ldg(table + i);
+    return p < 0 ? -2 : p;
 }
 
 // The keys that some position of [p0, p1] sees, as two ranges [0, sink_end)
@@ -91,8 +94,9 @@ struct Tiles {
     __host__ __device__ __forceinline__ int key0(int i) const { return (i < n_sink ? i : first + i - n_sink) * T; }
 };
 
-// Whether the 16 keys from k0 on hold a key of the span (a page without one is
-// not looked up: a sliding window's caller may have given it back).
+// Whether the 16 keys from k0 on hold a key of the span.  (A page without one is
+// not looked up: a sliding window's caller may have given it back.  Places of a
+// page that no row sees may hold anything, a NaN scale too.)
 __device__ __forceinline__ bool group_seen(const Span& s, int k0) {
     return k0 < s.hi && (k0 + kGroup > s.lo || k0 < s.sink_end);
 }
@@ -116,7 +120,7 @@ struct AttnArgs {
     const uint8_t* q;  // bf16 [n_rows][heads][d], ld_q elements between rows
     uint8_t* o;
     int64_t ld_q, ld_o;
-    int heads, group, window, sinks, max_rows;
+    int group, window, sinks, max_rows;
     int row_tiles;  // units of the most rows a sequence may have
     float scale_log2;
     int4* cut;        // [workers]: (pieces of the unit that it begins and does not end, or 0; its pair, head)

@@ -129,14 +129,13 @@ struct PartKV {
 };
 
 // What the page table lists for key `row` of tile i (looked at only when its
-// bytes are fetched): -1 when no row of the unit sees its group of keys or it
-// lies behind the last key, -2 behind the table's end.
+// bytes are fetched), -1 when no row of the unit sees it.
 __device__ __forceinline__ int lookup(const View& v, const int32_t* table, const Piece& w, const Tiles<kKeys>& tiles, int i,
                                       int row) {
     const int key = tiles.key0(i) + row;
-    if (i >= w.end || key >= w.rows.span.hi || !group_seen(w.rows.span, key & ~(kGroup - 1))) return -1;
-    const int j = v.page_shift >= 0 ? key >> v.page_shift : key / v.page_size;
-    return j < v.max_pages ? __ldg(table + j) : -2;
+    const Span& s = w.rows.span;
+    if (i >= w.end || key >= s.hi || (key < s.lo && key >= s.sink_end)) return -1;
+    return listed(table, v.page_shift >= 0 ? key >> v.page_shift : key / v.page_size);
 }
 
 template <int D>
@@ -394,7 +393,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
         const int64_t orow = w.s.first + f / a.group;
         const int qh = w.head * a.group + f % a.group;
         const int64_t slot = (int64_t)w.slot * kChunkRows + f - w.f0;
-        const float inv_l = l > 0.0f ? __fdiv_rn(back, l) : 0.0f;  // a row that sees no key: zeros
+        const float inv_l = l == 0.0f ? 0.0f : __fdiv_rn(back, l);  // a row that sees no key: zeros
         if (w.slot >= 0 && real) a.part_ml[slot] = make_float2(m, l);
 #pragma unroll
         for (int c = 0; c < D / 32; c++) {

@@ -7,6 +7,7 @@ loaded, or no CUDA device is present, the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -368,6 +369,11 @@ def _launch_on(index: int, stream, fn, *args) -> int:
         return fn(*args, raw)
 
 
+def _allocating_for(stream):
+    """Tensors made under it belong to `stream` (the current one when none is given), which will use them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _same_device(device: torch.device, *ts) -> None:
     index = device.index
     for t in ts:
@@ -391,7 +397,8 @@ def gemv(x: torch.Tensor, w: NVFP4Tensor, *, out: torch.Tensor | None = None, ou
     if K != w.cols or sx != 1:
         raise ValueError("gemv takes x [M, K] with unit column stride and K of the weight")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        with _allocating_for(stream):
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     elif out.dtype != torch.bfloat16 or out.shape != (M, N):
         raise ValueError("out is bf16 [M, N]")
     ldy, sy = out.stride()
@@ -614,10 +621,12 @@ class PagedKVCache:
     def gather(self, rows: PagedRows, *, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
                ws: torch.Tensor | None = None, stream=None):
         """Read the rows' K and V back to bf16 [n_rows, kv_heads, d]."""
-        if k_out is None:
-            k_out = torch.empty((rows.n_rows, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
-        if v_out is None:
-            v_out = torch.empty_like(k_out, memory_format=torch.contiguous_format)
+        shape = (rows.n_rows, self.kv_heads, self.head_dim)
+        with _allocating_for(stream):
+            if k_out is None:
+                k_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            if v_out is None:
+                v_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
         heads = self.kv_heads
         ld_k, ld_v = self._row_stride(rows, heads, k_out), self._row_stride(rows, heads, v_out)
         ws = self.ws_rows if ws is None else ws
@@ -628,7 +637,7 @@ class PagedKVCache:
         return k_out, v_out
 
     def attention_workspace(self, rows: PagedRows, heads: int, *, window: int = 0, sinks: int = 0) -> torch.Tensor:
-        """A workspace for attention() with these arguments (and for any with fewer rows of the same bounds)."""
+        """A workspace for attention() with these arguments; calls that may run at the same time take one each."""
         n = int(lib().nvfp4_paged_attention_workspace_bytes(self._ref, rows._ref, heads, window, sinks))
         if n == 0:
             raise ValueError("nvfp4_paged_attention_workspace_bytes: refused arguments")
@@ -643,11 +652,12 @@ class PagedKVCache:
         if q.dim() != 3:
             raise ValueError("attention takes q [n_rows, heads, head_dim]")
         heads = q.shape[1]
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        with _allocating_for(stream):
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if ws is None:
+                ws = self.attention_workspace(rows, heads, window=window, sinks=sinks)
         ld_q, ld_o = self._row_stride(rows, heads, q), self._row_stride(rows, heads, out)
-        if ws is None:
-            ws = self.attention_workspace(rows, heads, window=window, sinks=sinks)
         st = _launch_on(self.index, stream, lib().nvfp4_paged_attention, self._ref, rows._ref, q.data_ptr(), ld_q,
                         heads, window, sinks, scale, out.data_ptr(), ld_o, ws.data_ptr(), ws.numel())
         if st:

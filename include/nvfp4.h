@@ -277,9 +277,10 @@ nvfp4_status nvfp4_gemm(const nvfp4_tensor* A, const nvfp4_tensor* B, void* c_bf
  * ep->debug_y receives y as binary32 [m x N].  The requant and out_amax fields
  * must be unset (NVFP4_ERR_UNSUPPORTED) and debug_flags 0.  ep may be NULL.
  * Products of binary16 operands: e2m1 * s is exact there; a row of x is scaled
- * by a power of two per 128 columns, which rounds only values below 2^-28 of
- * the largest of them.  Binary32 sums in a fixed order.  One launch, no
- * workspace. */
+ * by a power of two (a row whose activations do not fit in shared memory: each
+ * 128 columns by their own), which rounds only values below 2^-28 of the largest
+ * of them.  Binary32 sums in a fixed order.  A NaN stays in its row.  One
+ * launch, no workspace. */
 nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t m, int64_t ldx, const nvfp4_tensor* W, void* y_bf16, int64_t ldy,
                         const nvfp4_epilogue* ep, nvfp4_stream_t stream);
 
@@ -426,10 +427,11 @@ typedef struct {
  * which rows a launch covers; max_len only how many CTAs share the keys (a
  * longer sequence is still read whole).
  * Reported as NVFP4_ERR_DEVICE (info = the sequence): a row range that is not
- * ascending within [0, n_rows], a negative length, and for the attention more
- * than max_rows rows (the sequence is skipped); a page entry that is needed and
- * is not one of the cache's pages, or lies behind max_pages (its rows are
- * skipped; the attention of that sequence is then not meaningful). */
+ * ascending within [0, n_rows], a length that is negative or above max_pages *
+ * page_size (or 2^30), and for the attention more than max_rows rows (the
+ * sequence is skipped); a page entry that is needed and is not one of the
+ * cache's pages (its rows are skipped; the attention of that sequence is then
+ * not meaningful). */
 typedef struct {
     const int32_t* row_start; /* [n_seqs + 1] */
     const int32_t* lens;      /* [n_seqs] */
@@ -467,7 +469,8 @@ nvfp4_status nvfp4_paged_gather(const nvfp4_paged_cache* cache, const nvfp4_page
  * the exact e2m1 * s * a32; queries are scaled by a power of two to binary16;
  * binary32 accumulation and softmax; the weights go to the second product in
  * binary16.  A row that sees no key gives zeros.  Pages that hold no visible
- * key are not looked up, so a window's caller may have given them back.
+ * key are not looked up, so a window's caller may have given them back; places
+ * that no row sees may hold any bytes.  A NaN query gives NaN, in its row alone.
  * workspace: nvfp4_paged_attention_workspace_bytes of the same arguments (0:
  * refused; at most 40 MB); results do not depend on what it
  * holds behind the control block.  Up to 16 (row, query head) pairs a K/V head
@@ -476,7 +479,9 @@ nvfp4_status nvfp4_paged_gather(const nvfp4_paged_cache* cache, const nvfp4_page
  * NVFP4_ERR_TIMEOUT (info = which wait) and leaves o incomplete.  Both deal the
  * key tiles out in equal runs, whatever the lengths, and a second launch joins
  * the rows whose keys lie in several runs; decode steps whose spans (max_len, or
- * window and sinks) are below 2048 keys take one launch. */
+ * window and sinks) are below 2048 keys take one launch.  max_rows decides for
+ * all sequences of a call: decode steps among long chunks run faster in a call
+ * of their own. */
 size_t nvfp4_paged_attention_workspace_bytes(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows,
                                              int32_t heads, int32_t window, int32_t sinks);
 nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows, const void* q_bf16,

@@ -135,6 +135,57 @@ def test_captured_and_on_another_stream():
     assert torch.equal(out, nv.gemv(x, w))
 
 
+@pytest.mark.parametrize("m,k", [(3, 512), (5, 32768), (16, 640), (16, 16384)])
+def test_what_is_not_finite_stays_in_its_row(m, k):
+    require_gpu()
+    w, _ = _weight(200, k, seed=k)
+    x = dev_bf16(syn.activations_bf16(m, k, seed=m))
+    want = nv.gemv(x, w)
+    for bad in (float("nan"), float("inf")):
+        y = x.clone()
+        y[1, 77] = bad
+        got = nv.gemv(y, w)
+        assert not torch.any(torch.isfinite(got[1]))
+        got[1] = want[1]
+        assert torch.equal(got, want)
+
+
+def test_offsets_beyond_32_bits():
+    """A weight of more than 4 GiB of codes, block scales all 1."""
+    require_gpu()
+    n, k, m = (1 << 20) + 150, 8192, 9
+    w = nv.empty_nvfp4(n, k)
+    assert w.codes.numel() > 1 << 32
+    w.codes.zero_()
+    w.scales.fill_(0x38)
+    w.global_scale.fill_(0.125)
+    rows = np.r_[0:3, n - 200:n]
+    codes = np.random.default_rng(5).integers(0, 256, (rows.size, k // 2), dtype=np.uint8)
+    w.codes[torch.from_numpy(rows).cuda()] = torch.from_numpy(codes).cuda()
+    level = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6])
+    wf = 0.125 * np.stack((level[codes & 15], level[codes >> 4]), -1).reshape(rows.size, k)
+    xb = syn.activations_bf16(m, k, seed=3)
+    x = bf16_to_f64(xb)
+    y32 = torch.empty((m, n), dtype=torch.float32, device="cuda")
+    out = nv.gemv(dev_bf16(xb), w, out_f32=y32)
+    at = torch.from_numpy(rows).cuda()
+    _check(y32[:, at], out[:, at], x @ wf.T, _bound(x, wf))
+    assert not torch.any(out[:, 3:n - 200])
+
+
+def test_given_streams():
+    require_gpu()
+    w, _ = _weight(1000, 2048, seed=1)
+    xs = [dev_bf16(syn.activations_bf16(m, 2048, seed=m)) for m in (1, 4, 16)]
+    want = [nv.gemv(x, w) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [(nv.gemv(x, w, stream=s), y) for _ in range(4) for x, s, y in zip(xs, streams, want)]
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a, b)
+
+
 def test_python_refusals():
     require_gpu()
     w, _ = _weight(64, 128, seed=3)

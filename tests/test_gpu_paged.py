@@ -439,6 +439,133 @@ def test_python_refusals():
         s.cache.attention(r, torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda"), ws=s.cache.ws_rows[:128])
 
 
+@pytest.mark.parametrize("d,page", [(64, 16), (64, 48), (128, 4112), (128, 64)])
+@pytest.mark.parametrize("counts,heads", [([1, 1, 1, 1], 8), ([2, 1, 2, 0], 8), ([1, 1, 1, 1], 12), ([3, 1, 3, 3], 5)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2500, 40)])
+def test_long_decode_steps(d, page, counts, heads, window, sinks):
+    """Spans of 2048 keys and more, with up to 8 and up to 16 (row, head) pairs; short sequences among them."""
+    require_gpu()
+    s = Setup([2100, 37, 5003, 3], counts, 1, d, page, seed=page + heads).fill()
+    _attend(s, heads, window=window, sinks=sinks, seed=heads)
+
+
+@pytest.mark.parametrize("count", [1, 2])
+@pytest.mark.parametrize("max_len", [0, 40])
+def test_lengths_beyond_the_hosts_bound(count, max_len):
+    """max_len says only how the work is dealt out."""
+    require_gpu()
+    s = Setup([3001, 40, 200], [count] * 3, 2, 64, 16, seed=41).fill()
+    _attend(s, 16, rows=s.rows(max_len=max_len), seed=4)
+    _attend(s, 16, rows=s.rows(max_len=max_len), window=77, sinks=9, seed=4)
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [9, 1]])
+def test_many_heads_of_one_key(counts):
+    """A group of 71 heads: a unit's rows begin and end inside a token."""
+    require_gpu()
+    s = Setup([500, 33], counts, 1, 64, 16, seed=42).fill()
+    _attend(s, 71, seed=5)
+    _attend(s, 71, window=20, sinks=2, seed=5)
+
+
+@pytest.mark.parametrize("length,window,sinks,count", [(100, 10, 0, 1), (100, 13, 3, 2), (333, 50, 19, 3),
+                                                       (5000, 3000, 7, 1), (5001, 2999, 33, 2), (300, 37, 5, 70)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_places_that_no_row_sees_may_hold_anything(length, window, sinks, count, d):
+    """Also those that share a page, or 16 keys, with visible ones: NaN scales there change nothing."""
+    require_gpu()
+    page = 64
+    s = Setup([length], [count], 2, d, page, seed=43).fill()
+    want = _attend(s, 4, window=window, sinks=sinks, seed=7)
+    first = length - count - window + 1
+    assert first > sinks
+    for pos in range(sinks, first):
+        p, o = int(s.table[0, pos // page]), pos % page
+        for t in (s.cache.k_codes, s.cache.k_scales, s.cache.v_codes, s.cache.v_scales):
+            t[p, :, o] = 0xFF
+    assert torch.equal(_attend(s, 4, window=window, sinks=sinks, seed=7), want)
+
+
+@pytest.mark.parametrize("length,count", [(60, 1), (3000, 2), (3000, 60)])
+def test_entries_below_zero_are_reported(length, count):
+    """-1, which also stands for a page given back, is no page where one is needed; lengths that the table does not
+    reach are refused before they make work."""
+    require_gpu()
+    s = Setup([40, length], [1, count], 1, 64, 16, seed=44).fill()
+    q = dev_bf16(syn.normal_bf16((s.n_rows, 2, 64), seed=1))
+    for entry in (-1, -7, s.cache.n_pages, 2 ** 31 - 1):
+        table = s.table.copy()
+        table[1, 1] = entry
+        rows = s.rows(table=table)
+        ws = s.cache.attention_workspace(rows, 2)
+        s.cache.attention(rows, q, ws=ws)
+        assert nv.read_device_error(ws) == (nv.ERR_DEVICE, 1)
+    for n in (16 * s.table.shape[1] + 1, 2 ** 31 - 1):
+        rows = s.rows(lens=[40, n], max_len=length)
+        out = torch.full_like(q, 5.0)
+        ws = s.cache.attention_workspace(rows, 2)
+        s.cache.attention(rows, q, ws=ws, out=out)
+        assert nv.read_device_error(ws) == (nv.ERR_DEVICE, 1)
+        assert torch.all(out[1:] == 5.0) and not torch.any(out[0] == 5.0)
+
+
+@pytest.mark.parametrize("length,count", [(60, 2), (3000, 2), (9000, 60)])
+def test_a_nan_query_stays_in_its_row(length, count):
+    require_gpu()
+    s = Setup([length], [count], 2, 128, 16, seed=45).fill()
+    q = dev_bf16(syn.normal_bf16((count, 8, 128), seed=2))
+    want = s.cache.attention(s.rows(), q).clone()
+    q[count - 1, 3, 77] = float("nan")
+    got = s.cache.attention(s.rows(), q)
+    assert torch.all(torch.isnan(got[count - 1, 3]))
+    want[count - 1, 3] = got[count - 1, 3] = 0
+    assert torch.equal(got, want)
+
+
+def test_calls_at_the_same_time_and_given_streams():
+    """Two streams, each with workspaces of its own, given and made by the calls."""
+    require_gpu()
+    s = Setup([5000, 700], [1, 1], 2, 128, 32, seed=46).fill()
+    c = Setup([900, 64], [300, 64], 2, 128, 32, seed=47).fill()
+    q = dev_bf16(syn.normal_bf16((s.n_rows, 8, 128), seed=1))
+    qc = dev_bf16(syn.normal_bf16((c.n_rows, 8, 128), seed=2))
+    rows, rows_c = s.rows(), c.rows()
+    want, want_c = s.cache.attention(rows, q), c.cache.attention(rows_c, qc)
+    kv, kv_c = s.cache.gather(rows), c.cache.gather(rows_c)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        got += [(s.cache.attention(rows, q, stream=a), want), (c.cache.attention(rows_c, qc, stream=b), want_c)]
+        got += list(zip(s.cache.gather(rows, stream=b), kv)) + list(zip(c.cache.gather(rows_c, stream=a), kv_c))
+    torch.cuda.synchronize()
+    for x, w in got:
+        assert torch.equal(x, w)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages behind the first 4 GiB of codes."""
+    require_gpu()
+    kv, d, page = 8, 128, 64
+    n_pages = (1 << 32) // (kv * page * d // 2) + 40
+    cache = nv.PagedKVCache(n_pages, page, kv, d, k_scale=K_SCALE, v_scale=V_SCALE)
+    assert cache.k_codes.numel() > 1 << 32
+    n = 20 * page + 5
+    s = Setup([n], [n], kv, d, page, seed=48)
+    table = _i32(n_pages - 1 - np.arange(21)[None])
+    s.table = table.cpu().numpy()
+    s.cache = cache
+    s.fill()
+    for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
+        assert not torch.any(t[:n_pages - 21]) and torch.any(t[n_pages - 21])
+    _attend(s, 8, seed=1)
+    s.counts, s.start, s.n_rows = [1], np.array([0, 1]), 1
+    _attend(s, 16, seed=2)
+    k, v = cache.gather(s.rows(counts=[n]))
+    for got, x, a in ((k, s.k, K_SCALE), (v, s.v, V_SCALE)):
+        assert np.array_equal(host_bits(got).reshape(-1, d), oracle.dequant_bf16(*oracle.quantize(x[0].reshape(-1, d), alpha=a)))
+
+
 # ---- the operators together ------------------------------------------------------------------------------------------
 def test_decoding_a_sequence_token_by_token():
     """A one-layer causal decoder on the operators: a prompt of 21 tokens as one chunk, then 12 single tokens, two
