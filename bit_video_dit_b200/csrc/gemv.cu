@@ -10,10 +10,11 @@
 // One CTA an SM takes an equal share of the weight's groups of 16 rows.  Four
 // groups {32 i + 16 half + 0..15} of a 128-row scale tile make a quad: the tile
 // layout has the scales of four such rows in 16 consecutive bytes.  The warps
-// split K in chunks of 128 columns and take two or three quads of rows at a time,
-// so that a chunk's activations serve 128 rows.  The weight's bytes pass
-// through a ring of (quad, chunk) pieces in shared memory a warp, which runs on
-// across passes: 70 to 110 KB an SM on the way, and no registers wait.
+// split K in chunks of 128 columns and take three or four quads of rows at a
+// time (a pass), so that a chunk's activations serve up to 256 rows.  The
+// weight's bytes pass through a ring of (quad, chunk) pieces in shared memory a
+// warp, which runs on across passes: 70 to 110 KB an SM on the way, and no
+// registers wait.
 // In a piece lane (g, t) reads 16 bytes (32 consecutive columns, two scale
 // blocks) of rows g and g + 8 of each group; the columns of the 16 x 8 x 16
 // matrix instruction are permuted so that these are its own A fragments, and
@@ -25,6 +26,16 @@
 // memory and the power comes off at the end; else a chunk's activations pass
 // through the ring before its pieces and have a power of their own, which comes
 // off the chunk's sums.
+//
+// Measured: 28672 x 8192 (132 MB) 32 us with one row (4.1 TB/s), 40 with 8, 51
+// with 16; 14336 x 4096 12.6, 14, 19.  What bounds it is the conversion and
+// integer pipe, with the issue slots half full: decoding a pair of codes takes
+// 3.6 cycles of a scheduler, which alone is 14 us of that weight, and scaling the
+// activations, addresses and scale bytes the rest; hence few, large passes.
+// Measured and not taken, 16 rows of that weight: decoding into tensor memory as
+// the A operand of tcgen05 products (97 us: 61 cycles a 128 x 16 x 16 product, and
+// the pieces' addresses a lane), 12 warps and two quads a pass (52), pairs of
+// groups interleaved there (56; with one row of eight it gains: 35 -> 32).
 #include <cstdint>
 
 #include "fp4mma.cuh"
@@ -40,14 +51,22 @@ constexpr int kPiece = 64 * 64 + 2 * 16 * 16;  // a piece's codes, then its scal
 constexpr int kMaxM = 16;
 constexpr int kPitch = 64 + 4;  // of the partial sums' rows: the fragment stores spread over all banks
 
-// Up to 8 rows (NT = 1): 16 warps of 128 registers, two pieces a ring; up to 16
-// rows: 12 of 168, three pieces.  (What the accumulators leave room for.)
+// Up to 8 rows (NT = 1): 16 warps of 128 registers, three quads a pass, two
+// pieces a ring; up to 16 rows: 8 warps of 255, four quads, four pieces, since
+// scaling a chunk's activations costs as much as a quad's products and is done
+// once a pass (14336 x 4096, 16 rows: 21 -> 19 us against 12 warps and two quads).
 template <int NT>
 struct Cfg {
-    static constexpr int kWarps = NT == 1 ? 16 : 12, kThreads = kWarps * 32, kStages = NT == 1 ? 2 : 3;
-    static constexpr int kQuads = NT == 1 ? 3 : 2;  // of a pass
+    static constexpr int kWarps = NT == 1 ? 16 : 8, kThreads = kWarps * 32, kStages = NT == 1 ? 2 : 4;
+    static constexpr int kQuads = NT == 1 ? 3 : 4;  // of a pass
     static constexpr int kRing = kWarps * kStages * kPiece, kPart = kWarps * 8 * NT * kPitch * 4;
     static constexpr int kX = 227 * 1024 - 256 - kRing - kPart;  // what is left for activations
+};
+
+// A number known when compiling, as an argument.
+template <int N>
+struct Int {
+    static constexpr int value = N;
 };
 
 struct Args {
@@ -73,14 +92,25 @@ __device__ __forceinline__ uint4 lds16(uint32_t p) {
     return v;
 }
 
-// Quad q's groups 4 q + lo .. 4 q + hi - 1 belong to the CTA; its row 16 i + r
-// is row `row0` + 32 i + r of the weight.
+// What a CTA computes: `whole` quads from quad0 on, then the groups [g0, g1),
+// its share of those that whole quads for every CTA leave over.  (Groups dealt
+// out without regard to the quads: a CTA's 12 lay in four of them, and a piece's
+// overhead is per quad.)
+struct Share {
+    int quad0, whole, g0, g1;
+    __device__ __forceinline__ int count() const { return whole + (g1 > g0 ? (g1 - 1) / 4 - g0 / 4 + 1 : 0); }
+};
+
+// The CTA's q-th quad: of its rows 16 i + r, i in [lo, hi) belong to the CTA and
+// are rows `row0` + 32 i + r of the weight.
 struct Quad {
     int row0, lo, hi;
-    __device__ __forceinline__ Quad(int q, int g0, int g1) {
+    __device__ __forceinline__ Quad(const Share& s, int i) {
+        const bool full = i < s.whole;
+        const int q = full ? s.quad0 + i : s.g0 / 4 + i - s.whole;
         row0 = (q >> 1) * 128 + (q & 1) * 16;
-        lo = max(0, g0 - 4 * q);
-        hi = min(4, g1 - 4 * q);
+        lo = full ? 0 : max(0, s.g0 - 4 * q);
+        hi = full ? 4 : min(4, s.g1 - 4 * q);
     }
 };
 
@@ -124,11 +154,11 @@ __device__ __forceinline__ int x_place(int r, int j) { return (j & ~3) | ((j ^ (
 
 // A chunk's activations (bf16) into a ring slot, the pieces of a row placed as above; columns behind K are zeros.
 __device__ __forceinline__ void load_x(const Args& a, int c, int lane, uint32_t dst) {
-    for (int i = lane; i < a.m * 16; i += 32) {
-        const int m = i >> 4, j = i & 15, col = c * kChunk + 8 * j;
-        const bool real = col < a.k;
-        copy16(dst + m * 256 + x_place(m, j) * 16, real ? a.x + ((int64_t)m * a.ldx + col) * 2 : a.x, real);
-    }
+    const int r = lane >> 4, j = lane & 15, col = c * kChunk + 8 * j;
+    const bool real = col < a.k;
+    const uint8_t* p = a.x + ((int64_t)r * a.ldx + (real ? col : 0)) * 2;
+    const uint32_t d = dst + r * 256 + x_place(r, j) * 16;  // (rows 2 on: the same place)
+    for (int m = 0; m + r < a.m; m += 2, p += a.ldx * 4) copy16(d + m * 256, p, real);
 }
 
 // 32 codes of one row with their two block scales -> 16 operand pairs
@@ -158,20 +188,24 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) gemv_kernel(const __grid
     const uint32_t xs = smem_u32(smem) + Cfg<NT>::kRing + Cfg<NT>::kPart;
     if (threadIdx.x < kMaxM) row_max[threadIdx.x] = 0u;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // the CTA's groups [g0, g1) and their quads [first, last]
-    const int g0 = (int)((int64_t)a.groups * blockIdx.x / gridDim.x), g1 = (int)((int64_t)a.groups * (blockIdx.x + 1) / gridDim.x);
-    if (g0 >= g1) return;
-    const int first = g0 / 4, last = (g1 - 1) / 4;
+    Share share;
+    share.whole = a.groups / 4 / (int)gridDim.x;
+    share.quad0 = share.whole * (int)blockIdx.x;
+    const int spread = share.whole * (int)gridDim.x * 4, rest = a.groups - spread;  // rest < 4 gridDim.x
+    share.g0 = spread + rest * (int)blockIdx.x / (int)gridDim.x;
+    share.g1 = spread + rest * ((int)blockIdx.x + 1) / (int)gridDim.x;
+    const int quads = share.count();
+    if (quads == 0) return;
 
     // the next piece to fetch: pass by pass, chunk by chunk, (the chunk's activations, then) quad by quad
     constexpr int kBefore = XS ? 0 : 1;
-    int f_quad = first - kBefore, f_pass = first, f_chunk = warp, f_slot = 0;
+    int f_quad = -kBefore, f_pass = 0, f_chunk = warp, f_slot = 0;
     auto fetch = [&]() {
-        if (f_chunk < a.chunks && f_pass <= last) {
+        if (f_chunk < a.chunks && f_pass < quads) {
             if (!XS && f_quad < f_pass) load_x(a, f_chunk, lane, ring + (uint32_t)(f_slot * kPiece));
-            else load_piece(a, Quad(f_quad, g0, g1), f_chunk, lane, ring + (uint32_t)(f_slot * kPiece));
+            else load_piece(a, Quad(share, f_quad), f_chunk, lane, ring + (uint32_t)(f_slot * kPiece));
             f_slot = f_slot == kStages - 1 ? 0 : f_slot + 1;
-            if (++f_quad > min(last, f_pass + kQuads - 1)) {
+            if (++f_quad >= min(quads, f_pass + kQuads)) {
                 f_chunk += kWarps;
                 if (f_chunk >= a.chunks) {
                     f_chunk = warp;
@@ -234,7 +268,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) gemv_kernel(const __grid
         slot = slot == kStages - 1 ? 0 : slot + 1;
         return at;
     };
-    for (int pass = first; pass <= last; pass += kQuads) {
+    for (int pass = 0; pass < quads; pass += kQuads) {
         float acc[kQuads][NT][4][4];
 #pragma unroll
         for (int q = 0; q < kQuads; q++)
@@ -266,39 +300,69 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) gemv_kernel(const __grid
             }
 #pragma unroll
             for (int q = 0; q < kQuads; q++) {
-                if (pass + q > last) continue;
-                const Quad quad(pass + q, g0, g1);
+                if (pass + q >= quads) continue;
+                const Quad quad(share, pass + q);
                 const uint32_t at = next_piece();
-                const uint32_t scales = at + 64 * 64 + (t >> 1) * 256 + g * 16;
+                const uint32_t scales = at + 64 * 64 + (t >> 1) * 256 + g * 16, codes = at + g * 64 + 16 * t;
                 const uint4 s0 = lds16(scales), s1 = lds16(scales + 8 * 16);
+                const int sh = 16 * (t & 1);
+                const uint32_t sc[4][2] = {
+                    {s0.x >> sh, s1.x >> sh}, {s0.y >> sh, s1.y >> sh}, {s0.z >> sh, s1.z >> sh}, {s0.w >> sh, s1.w >> sh}};
+                // groups first .. first + number - 1, interleaved so that no product waits for the one before it
+                auto groups = [&](auto first, auto number) {
+                    constexpr int i0 = decltype(first)::value, n = decltype(number)::value;
+                    uint4 c[n][2];
+                    __half2 s[n][2];
+                    float chunk[XS ? 1 : n][NT][4];
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    if (i < quad.lo || i >= quad.hi) continue;
-                    const uint32_t codes = at + (16 * i + g) * 64 + 16 * t;
-                    uint32_t w0[16], w1[16];
-                    decode32(lds16(codes), (i == 0 ? s0.x : i == 1 ? s0.y : i == 2 ? s0.z : s0.w) >> (16 * (t & 1)), w0);
-                    decode32(lds16(codes + 8 * 64), (i == 0 ? s1.x : i == 1 ? s1.y : i == 2 ? s1.z : s1.w) >> (16 * (t & 1)),
-                             w1);
+                    for (int i = 0; i < n; i++)
 #pragma unroll
-                    for (int j = 0; j < NT; j++) {
-                        float chunk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        float* d = XS ? acc[q][j][i] : chunk;
+                        for (int h = 0; h < 2; h++) {
+                            c[i][h] = lds16(codes + (16 * (i0 + i) + 8 * h) * 64);
+                            s[i][h] = e4m3x2_to_half2((uint16_t)sc[i0 + i][h]);
+                        }
 #pragma unroll
-                        for (int e = 0; e < 8; e++)
-                            mma_16816(d, w0[2 * e], w1[2 * e], w0[2 * e + 1], w1[2 * e + 1], xb[j][2 * e],
-                                      xb[j][2 * e + 1]);
-                        if (!XS)
+                    for (int w = 0; w < 4; w++)
 #pragma unroll
-                            for (int e = 0; e < 4; e++) acc[q][j][i][e] = fmaf(d[e], down[j][e & 1], acc[q][j][i][e]);
-                    }
+                        for (int i = 0; i < n; i++) {
+                            uint32_t w0[4], w1[4];
+                            auto word = [&](const uint4& v) { return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w; };
+                            decode8(word(c[i][0]), w < 2 ? __low2half2(s[i][0]) : __high2half2(s[i][0]), w0);
+                            decode8(word(c[i][1]), w < 2 ? __low2half2(s[i][1]) : __high2half2(s[i][1]), w1);
+#pragma unroll
+                            for (int e = 0; e < 2; e++)
+#pragma unroll
+                                for (int j = 0; j < NT; j++) {
+                                    float* d = XS ? acc[q][j][i0 + i] : chunk[XS ? 0 : i][j];
+                                    const uint32_t b0 = xb[j][4 * w + 2 * e], b1 = xb[j][4 * w + 2 * e + 1];
+                                    if (!XS && w == 0 && e == 0) mma_16816_first(d, w0[0], w1[0], w0[1], w1[1], b0, b1);
+                                    else mma_16816(d, w0[2 * e], w1[2 * e], w0[2 * e + 1], w1[2 * e + 1], b0, b1);
+                                }
+                        }
+                    if (!XS)
+#pragma unroll
+                        for (int i = 0; i < n; i++)
+#pragma unroll
+                            for (int j = 0; j < NT; j++)
+#pragma unroll
+                                for (int e = 0; e < 4; e++)
+                                    acc[q][j][i0 + i][e] = fmaf(chunk[XS ? 0 : i][j][e], down[j][e & 1], acc[q][j][i0 + i][e]);
+                };
+                if (NT == 1 && quad.lo == 0 && quad.hi == 4) {
+                    groups(Int<0>{}, Int<4>{});
+                } else {
+                    if (quad.lo <= 0 && quad.hi > 0) groups(Int<0>{}, Int<1>{});
+                    if (quad.lo <= 1 && quad.hi > 1) groups(Int<1>{}, Int<1>{});
+                    if (quad.lo <= 2 && quad.hi > 2) groups(Int<2>{}, Int<1>{});
+                    if (quad.lo <= 3 && quad.hi > 3) groups(Int<3>{}, Int<1>{});
                 }
             }
         }
         // the warps' sums, in a fixed order, and the epilogue
 #pragma unroll
         for (int q = 0; q < kQuads; q++) {
-            if (pass + q > last) continue;
-            const Quad quad(pass + q, g0, g1);
+            if (pass + q >= quads) continue;
+            const Quad quad(share, pass + q);
 #pragma unroll
             for (int j = 0; j < NT; j++)
 #pragma unroll
@@ -399,7 +463,7 @@ extern "C" nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t m, int64_t ldx, c
     cfg.gridDim = dim3((unsigned)(a.groups < gemv::kSms ? a.groups : gemv::kSms));
     const bool two = m > 8;
     const int64_t xbytes = (int64_t)a.chunks * m * 256, room = two ? gemv::Cfg<2>::kX : gemv::Cfg<1>::kX;
-    const bool xs = xbytes <= room;  // (then at most 100 or 33 parts, of the 128 or 48 that the warps hold)
+    const bool xs = xbytes <= room;  // (then at most 102 or 106 parts, of the 128 or 112 that the warps hold)
     cfg.blockDim = dim3((unsigned)(two ? gemv::Cfg<2>::kThreads : gemv::Cfg<1>::kThreads));
     cfg.dynamicSmemBytes = (size_t)((two ? gemv::Cfg<2>::kRing + gemv::Cfg<2>::kPart
                                          : gemv::Cfg<1>::kRing + gemv::Cfg<1>::kPart) + (xs ? xbytes : 0));

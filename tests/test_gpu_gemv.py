@@ -2,10 +2,10 @@
 
 Bound of the binary32 result.  The operands are exact but for activations below 2^-28 of the largest of their row,
 which move by at most 2^-25 2^-14 of it (half a binary16 step at 2^-14, under a scale that puts the maximum at 2^14 or
-above).  A product passes through the 8 matrix instructions of each of a warp's chunks (12 or 16 warps share them) and
+above).  A product passes through the 8 matrix instructions of each of a warp's chunks (8 or 16 warps share them) and
 the sum of the warps.  An instruction sums 16 products and an accumulator and loses at most 18 units 2^-23 of their
 magnitudes:
-  |y - ref| <= (8 * 18 * ceil(chunks / 12) + 16) 2^-23 sum|x w| + 2^-39 max|x| sum|w|,
+  |y - ref| <= (8 * 18 * ceil(chunks / 8) + 16) 2^-23 sum|x w| + 2^-39 max|x| sum|w|,
 and the epilogue's own roundings, 2^-23 a step."""
 import numpy as np
 import pytest
@@ -28,7 +28,7 @@ def _weight(n, k, seed):
 
 def _bound(x, w):
     k = x.shape[1]
-    depth = 8 * 18 * -(-k // (128 * 12)) + 16
+    depth = 8 * 18 * -(-k // (128 * 8)) + 16
     return (depth * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T) +
             2.0 ** -39 * np.abs(x).max(1, keepdims=True) * np.abs(w).sum(1)[None])
 
