@@ -211,7 +211,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3) rows_kernel(const __grid_co
 // tiles in shared memory a warp, so that no registers wait for them.
 //
 // Bound: the cache's bytes (a key and value are 9/8 head_dim bytes a head),
-// and beside them the decoding (fp4mma.cuh).
+// and beside them the decoding (fp4mma.cuh).  64 sequences of 6000 keys on
+// average x 8 heads of 128 (177 MB): 49 us, of which the runs' beginnings and
+// ends (places, pages, queries; joining) are 12; the copies alone then take 27
+// (6.5 TB/s), the arithmetic alone 31, both 37.
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 32;  // keys of a tile
 constexpr int kSms = 148;
@@ -376,7 +379,19 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
     const CopyLane<D> ln(v, lane);
     const int32_t* table = v.pages + (int64_t)b * v.max_pages;
 
-    // Copies run kStages - 1 tiles ahead, page lookups one more.  A tile whose 32 keys are all seen by some row and
+    // queries: column n of tile j is row f0 + 8 j + n; columns past the last row are zeros and nobody reads them
+    uint4 raw[NT][D / 32];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+        const int f = f0 + 8 * j + g;
+        const bool in = 8 * j + g < rows.n;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((int64_t)(s.first + f / a.group) * a.ld_q + (int64_t)(head * a.group + f % a.group) * D + D / 4 * t) * 2);
+#pragma unroll
+        for (int i = 0; i < D / 32; i++) raw[j][i] = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+
+    // Copies run kStages - 1 tiles ahead.  A tile whose 32 keys are all seen by some row and
     // lie in one page (of 32 or more tokens) takes the short way.
     const Span& sp = rows.span;
     const int jump = tiles.first > tiles.n_sink ? tiles.n_sink * kKeys : -1, after_jump = tiles.first * kKeys;
@@ -384,16 +399,18 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
     auto whole = [&](int k0) {
         return v.page_shift >= 5 && ((k0 >= sp.lo && k0 + kKeys <= sp.hi) || k0 + kKeys <= sp.sink_end);
     };
-    int page0 = -1, page1 = -1;
-    auto lookup = [&](int k0) {
-        if (whole(k0)) {
-            page0 = page1 = listed(table, k0 >> v.page_shift);
-        } else {
-            page0 = group_page(v, table, sp, k0);
-            page1 = group_page(v, table, sp, k0 + kGroup);
+    // pages are looked up for 32 tiles at a time, a lane a tile
+    int listed0 = -1, listed1 = -1;
+    auto lookup = [&](int i) {
+        listed0 = listed1 = -1;
+        if (i + lane < end) {
+            const int k = tiles.key0(i + lane);
+            listed0 = group_page(v, table, sp, k);
+            listed1 = group_page(v, table, sp, k + kGroup);
         }
     };
-    auto fetch = [&](int k0, uint32_t dst) {
+    auto fetch = [&](int i, int k0, uint32_t dst) {
+        const int page0 = __shfl_sync(0xFFFFFFFFu, listed0, i), page1 = __shfl_sync(0xFFFFFFFFu, listed1, i);
         if (whole(k0) && (unsigned)page0 < (unsigned)v.n_pages) {
             load_whole_tile<D>(ln, (uint32_t)page0 * page_rows + head_row + (uint32_t)(k0 & (v.page_size - 1)), dst);
         } else {
@@ -404,32 +421,24 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
     const uint32_t ring_end = ring + kStages * Ring<D>::bytes;
     int ahead = begin, ahead_k0 = tiles.key0(begin);  // the next tile to fetch, its page already looked up
     uint32_t dst = ring;
-    if (ahead < end) lookup(ahead_k0);
+    lookup(begin);
     auto advance = [&]() {
         if (ahead < end) {
-            fetch(ahead_k0, dst);
+            fetch(ahead - begin, ahead_k0, dst);
             dst = dst + Ring<D>::bytes == ring_end ? ring : dst + Ring<D>::bytes;
             ahead_k0 = step(ahead_k0);
-            if (++ahead < end) lookup(ahead_k0);
+            if ((++ahead - begin) % 32 == 0) lookup(ahead);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll 1
     for (int i = 0; i < kStages - 1; i++) advance();
 
-    // queries: column n of tile j is row f0 + 8 j + n; columns past the last row are zeros and nobody reads them
     uint32_t qb[NT][D / 8];
     float c_col[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; j++) {
-        uint4 raw[D / 32];
-        const int f = f0 + 8 * j + g;
-        const bool in = 8 * j + g < rows.n;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + ((int64_t)(s.first + f / a.group) * a.ld_q + (int64_t)(head * a.group + f % a.group) * D + D / 4 * t) * 2);
-#pragma unroll
-        for (int i = 0; i < D / 32; i++) raw[i] = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-        const float down = scale_row<D / 32>(raw, qb[j]) * (__ldg(v.a32[0]) * a.scale_log2);
+        const float down = scale_row<D / 32>(raw[j], qb[j]) * (__ldg(v.a32[0]) * a.scale_log2);
 #pragma unroll
         for (int e = 0; e < 2; e++) c_col[j][e] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4 * e);
     }
@@ -628,7 +637,8 @@ constexpr int decode_ctas() {
     return kSms * (NT == 1 ? 3 : 2);
 }
 constexpr int kDecodeStages = 4;
-constexpr int kLeast = 8;  // tiles of a run: with fewer, joining many pieces takes longer (one sequence of 6000 keys: 36 us with 1, 21 with 8)
+constexpr int kLeast = 3;  // tiles of a run: fewer make many pieces to join, more few warps (one sequence of 6000 keys, 8
+                           // heads of 128: 17.4 us with 3, 18.1 with 4, 21 with 8; of 16000: 26 with 2, 22.8 with 3)
 template <int D>
 constexpr int decode_smem() {
     return kWarps * kDecodeStages * Ring<D>::bytes;
@@ -648,7 +658,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(co
     int4 cut = make_int4(0, 0, 0, 0);
     while (next_piece<8 * NT, kKeys>(a, run, u)) {
         decode_piece<D, NT, kDecodeStages>(a, u, ring, a.part_o, a.part_ml);
-        if (u.pieces) cut = make_int4(u.pieces, u.pair, u.head, 0);
+        if (u.pieces) cut = make_int4(u.pieces, u.pair, u.head, u.rows.n);
     }
     if ((threadIdx.x & 31) == 0) a.cut[run.worker] = cut;
 }
@@ -713,27 +723,39 @@ __global__ void __launch_bounds__(kUnitWarps * 32, NT == 1 ? 2 : 1) unit_kernel(
     }
 }
 
-// Joins the pieces of the unit that worker blockIdx.x began, a warp a row.
+// Joins the pieces of the unit that worker blockIdx.x began, a warp a row.  It is
+// loads that wait for loads (place, then weights and pieces together), so as many
+// as registers hold are on the way: one piece after the other it took 7 and 14 us
+// behind the decode steps of 64 and 4 sequences, 5 and 8 so.
 template <int D, int COLS>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnArgs a) {
     const View& v = a.v;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kBatch = COLS == kChunkRows ? 2 : 8;  // (a unit of chunks rarely lies in more than two runs)
     const int4 cut = __ldcg(a.cut + blockIdx.x);
     const int lane = threadIdx.x & 31, n = (int)blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (cut.x == 0) return;
-    const Seq s = load_seq(v, cut.y / a.row_tiles);
-    const int f = cut.y % a.row_tiles * COLS + n;
-    if (n >= COLS || f >= s.n * a.group) return;
+    if (cut.x == 0 || n >= cut.w) return;
+    const int first = __ldg(v.row_start + cut.y / a.row_tiles);  // (the worker has checked it)
     // piece 0 is the end of this worker's run, piece p the beginning of the p-th later one's
     auto at = [&](int p) { return (int64_t)(2 * ((int)blockIdx.x + p) + (p == 0)) * COLS + n; };
     float mx = kFloor, sum = 0.0f, y[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; e++) y[e] = 0.0f;
     for (int p0 = 0; p0 < cut.x; p0 += 32) {
-        // a lane has the weight of one piece
+        // a lane has the weight of one piece; kBatch pieces are on the way at a time
         const int count = min(32, cut.x - p0);
         const float2 ml = lane < count ? __ldcg(a.part_ml + at(p0 + lane)) : make_float2(kFloor, 0.0f);
+        float2 x[kBatch][D / 64];
+        auto load = [&](int p) {
+#pragma unroll
+            for (int u = 0; u < kBatch; u++)
+#pragma unroll
+                for (int e = 0; e < D / 64; e++)
+                    x[u][e] = p + u < count ? __ldcg(reinterpret_cast<const float2*>(a.part_o + at(p0 + p + u) * D) + 32 * e + lane)
+                                            : make_float2(0.0f, 0.0f);
+        };
+        load(0);
         float top = fmaxf(mx, ml.x);
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
@@ -745,19 +767,22 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
         sum = sum * before + add;
 #pragma unroll
         for (int e = 0; e < D / 32; e++) y[e] *= before;
-#pragma unroll 8
-        for (int p = 0; p < count; p++) {
-            const float wp = __shfl_sync(0xFFFFFFFFu, w, p);
+        for (int p = 0; p < count; p += kBatch) {
+            if (p > 0) load(p);
 #pragma unroll
-            for (int e = 0; e < D / 64; e++) {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(a.part_o + at(p0 + p) * D) + 32 * e + lane);
-                y[2 * e] += x.x * wp;
-                y[2 * e + 1] += x.y * wp;
+            for (int u = 0; u < kBatch; u++) {
+                const float wp = __shfl_sync(0xFFFFFFFFu, w, p + u);
+#pragma unroll
+                for (int e = 0; e < D / 64; e++) {
+                    y[2 * e] += x[u][e].x * wp;
+                    y[2 * e + 1] += x[u][e].y * wp;
+                }
             }
         }
     }
     const float f2 = sum == 0.0f ? 0.0f : __fdiv_rn(__ldg(v.a32[1]), sum);
-    const int64_t row = s.first + f / a.group, qh = cut.z * a.group + f % a.group;
+    const int f = cut.y % a.row_tiles * COLS + n;
+    const int64_t row = first + f / a.group, qh = cut.z * a.group + f % a.group;
     __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + (row * a.ld_o + qh * D) * 2);
 #pragma unroll
     for (int e = 0; e < D / 64; e++) dst[32 * e + lane] = __floats2bfloat162_rn(y[2 * e] * f2, y[2 * e + 1] * f2);

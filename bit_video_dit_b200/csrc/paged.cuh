@@ -123,7 +123,7 @@ struct AttnArgs {
     int group, window, sinks, max_rows;
     int row_tiles;  // units of the most rows a sequence may have
     float scale_log2;
-    int4* cut;        // [workers]: (pieces of the unit that it begins and does not end, or 0; its pair, head)
+    int4* cut;        // [workers]: (pieces of the unit that it begins and does not end, or 0; its pair, head, rows)
     float* part_o;    // [workers][2][cols][d] unnormalised
     float2* part_ml;  // [workers][2][cols] (reference maximum, sum)
 };

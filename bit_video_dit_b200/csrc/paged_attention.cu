@@ -481,7 +481,7 @@ __device__ __forceinline__ void mma_role(const AttnArgs& a, Shared& sh, uint32_t
     bool ok = true;
     Piece w;
     while (ok && next_piece<kChunkRows, kKeys>(a, run, w)) {
-        if (w.pieces) cut = make_int4(w.pieces, w.pair, w.head, 0);
+        if (w.pieces) cut = make_int4(w.pieces, w.pair, w.head, w.rows.n);
         const int count = max(0, w.end - w.begin);
         if (count == 0) continue;
         if (X == 1 && w.rows.n <= kTile) {  // no tile B: only the buffers' release

@@ -354,16 +354,17 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, *, out: torch.Tensor | None = None, bia
     return out
 
 
-# The current stream's handle by device index; torch.cuda.current_stream() makes an object each time, which takes
-# longer than the rest of a small call.
+# The current stream's handle by device index, and that device; torch.cuda.current_stream() makes an object each time,
+# which takes longer than the rest of a small call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _launch_on(index: int, stream, fn, *args) -> int:
     """Call fn(*args, stream) with device `index` current (its current stream when none is given)."""
     raw = _raw_stream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         return fn(*args, raw)
     with torch.cuda.device(index):
         return fn(*args, raw)
@@ -609,9 +610,9 @@ class PagedKVCache:
         if rope is not None:
             cos, sin = rope
             for t in rope:
-                if t.dtype != torch.float32 or t.shape != (rows.n_rows, self.head_dim // 2) or not t.is_contiguous():
-                    raise ValueError("rope tables are contiguous float32 [n_rows, d / 2]")
-            _same_device(self.device, cos, sin)
+                if (t.dtype != torch.float32 or t.shape != (rows.n_rows, self.head_dim // 2) or not t.is_contiguous() or
+                        t.get_device() != self.index):
+                    raise ValueError(f"rope tables are contiguous float32 [n_rows, d / 2] on {self.device}")
         ws = self.ws_rows if ws is None else ws
         st = _launch_on(self.index, stream, lib().nvfp4_paged_append, self._ref, rows._ref, k.data_ptr(), ld_k,
                         v.data_ptr(), ld_v, _ptr(cos), _ptr(sin), ws.data_ptr(), ws.numel())
