@@ -20,7 +20,8 @@
 // columns each) and O_A, O_B.  Scores are double-buffered: QK(j + 2) is issued
 // as soon as the softmax has read S of tile j, so that it finds the next tile's
 // done.  2640 rows x 24 heads over 23760 visible keys: 737 us with one buffer of
-// 128 keys and one issuing thread, 706 so (970 TFLOP/s of what the rows see).
+// 128 keys and one issuing thread, 706 so, 692 with rows read and written eight
+// lanes a line (990 TFLOP/s of what the rows see).
 // What is left is no unit's rate (products 1280 cycles of a tile's 2300,
 // exponentials 1024, issue 45%) but the hand-overs between the roles: without
 // the softmax's and the producers' work the same barriers take 640 us.
@@ -224,28 +225,68 @@ __device__ __forceinline__ void producer_role(const AttnArgs& a, Shared& sh, uin
 }
 
 // ---- softmax ---------------------------------------------------------------
-// Pair f of the unit's sequence into Q at row `row` (zeros past the last),
-// scaled by 2^k to binary16 (fp4mma.cuh); returns 2^-k.
+// The warp's 32 pairs from f on into Q at rows row0 .. (zeros past the last),
+// scaled by 2^k to binary16 (fp4mma.cuh); returns 2^-k of the lane's row.  Four
+// lanes read 64 bytes of a row together: a lane a row, the loads of 32 lines an
+// instruction took 2 us a unit, the stores of O below 4.
 template <int D>
-__device__ __forceinline__ float load_q_row(const AttnArgs& a, const Piece& w, uint32_t q_s, int f, int row) {
-    uint4 v[D / 8];
-    if (f < w.f0 + w.rows.n) {
+__device__ __forceinline__ float load_q_rows(const AttnArgs& a, const Piece& w, uint32_t q_s, int f, int row0) {
+    constexpr int kParts = D / 32;  // of 64 bytes
+    const int lane = threadIdx.x & 31, c = lane & 3;
+    uint4 v[4][kParts];
+    float down[4];
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+        const int fr = f + 8 * g + (lane >> 2);
+        const bool in = fr < w.f0 + w.rows.n;
         const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + ((int64_t)(w.s.first + f / a.group) * a.ld_q + (int64_t)(w.head * a.group + f % a.group) * D) * 2);
+            a.q + ((int64_t)(w.s.first + fr / a.group) * a.ld_q + (int64_t)(w.head * a.group + fr % a.group) * D) * 2) + c;
 #pragma unroll
-        for (int c = 0; c < D / 8; c++) v[c] = __ldg(src + c);
-    } else {
-#pragma unroll
-        for (int c = 0; c < D / 8; c++) v[c] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < kParts; i++) v[g][i] = in ? __ldg(src + 4 * i) : make_uint4(0u, 0u, 0u, 0u);
     }
-    const RowScale rs = row_scale(max_bits<D / 8>(v));
 #pragma unroll
-    for (int c = 0; c < D / 8; c++) {
-        uint32_t x[4];
-        scale8(v[c], rs.up, x);
-        st_shared16(q_s + c * 2048 + row * 16, make_uint4(x[0], x[1], x[2], x[3]));
+    for (int g = 0; g < 4; g++) {
+        uint32_t mx = max_bits<kParts>(v[g]);
+        mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+        const RowScale rs = row_scale(mx);
+        down[g] = rs.down;
+#pragma unroll
+        for (int i = 0; i < kParts; i++) {
+            uint32_t x[4];
+            scale8(v[g][i], rs.up, x);
+            st_shared16(q_s + (4 * i + c) * 2048 + (row0 + 8 * g + (lane >> 2)) * 16, make_uint4(x[0], x[1], x[2], x[3]));
+        }
     }
-    return rs.down;
+    float mine = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+        const float x = __shfl_sync(0xFFFFFFFFu, down[g], 4 * (lane & 7));
+        if (lane >> 3 == g) mine = x;
+    }
+    return mine;
+}
+
+// 128 bytes of each lane's row, by way of 4 KB of shared memory at `at`, to the
+// rows' places `dst` (NULL: none), so that eight lanes write a row's line.
+__device__ __forceinline__ void store_rows(uint32_t at, const uint32_t* x, uint8_t* dst) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        st_shared16(at + lane * 128 + ((i ^ (lane & 7)) << 4), make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+    __syncwarp();
+    const int c = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const int r = 4 * i + (lane >> 3);
+        uint4 y;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                     : "r"(at + r * 128 + ((c ^ (r & 7)) << 4)));
+        uint8_t* p = reinterpret_cast<uint8_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(dst), r));
+        if (p) *reinterpret_cast<uint4*>(p + 16 * c) = y;
+    }
+    __syncwarp();
 }
 
 // What a row sees of a tile: keys below `hi` that are at least `lo` or below
@@ -327,7 +368,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
         const bool real = f < w.f0 + w.rows.n;
         float c_s = 0.0f;
         if (w.begin < w.end) {  // (without a key tile the issuing thread does not wait for it)
-            c_s = load_q_row<D>(a, w, q_s, f, row) * ck;
+            c_s = load_q_rows<D>(a, w, q_s, f - (row & 31), row & ~31) * ck;
             fence_proxy_async_smem();
             mbar_arrive(&sh.q_full[X]);
         }
@@ -390,14 +431,19 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
             if (!got) return;
             tc_fence_after();
         }
-        const int64_t orow = w.s.first + f / a.group;
-        const int qh = w.head * a.group + f % a.group;
-        const int64_t slot = (int64_t)w.slot * kChunkRows + f - w.f0;
         const float inv_l = l == 0.0f ? 0.0f : __fdiv_rn(back, l);  // a row that sees no key: zeros
-        if (w.slot >= 0 && real) a.part_ml[slot] = make_float2(m, l);
-#pragma unroll
-        for (int c = 0; c < D / 32; c++) {
-            uint32_t r[32];
+        const int64_t slot = (int64_t)w.slot * kChunkRows + f - w.f0;
+        uint8_t* dst = nullptr;
+        if (real && w.slot >= 0) {
+            a.part_ml[slot] = make_float2(m, l);
+            dst = reinterpret_cast<uint8_t*>(a.part_o + slot * D);
+        } else if (real) {
+            dst = a.o + ((int64_t)(w.s.first + f / a.group) * a.ld_o + (int64_t)(w.head * a.group + f % a.group) * D) * 2;
+        }
+        // through P: no product reads it now, and the next unit's first P is written when all four warps have signalled
+        // q_full behind this
+        const uint32_t stage = p_s0 + (row >> 5) * 4096;
+        auto load_o = [&](int c, uint32_t* r) {
             if (!first) {
                 tmem_ld_32cols(t_o + 32 * c, r);
                 tmem_ld_wait();
@@ -406,26 +452,30 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
 #pragma unroll
                 for (int j = 0; j < 32; j++) r[j] = 0u;
             }
-            if (!real) continue;
-            if (w.slot >= 0) {
-                float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + 32 * c);
+        };
+        if (w.slot >= 0) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; c++) {
+                uint32_t r[32];
+                load_o(c, r);
+                store_rows(stage, r, dst ? dst + 128 * c : nullptr);
+            }
+        } else {
+#pragma unroll 1
+            for (int c = 0; c < D / 64; c++) {
+                uint32_t x[32];
 #pragma unroll
-                for (int g = 0; g < 8; g++)
-                    dst[g] = make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
-                                         __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
-            } else {
-                uint4* dst = reinterpret_cast<uint4*>(a.o + (orow * a.ld_o + (int64_t)qh * D + 32 * c) * 2);
+                for (int h = 0; h < 2; h++) {
+                    uint32_t r[32];
+                    load_o(2 * c + h, r);
 #pragma unroll
-                for (int g = 0; g < 4; g++) {
-                    uint32_t x[4];
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[8 * g + 2 * e]) * inv_l,
-                                                                       __uint_as_float(r[8 * g + 2 * e + 1]) * inv_l);
-                        x[e] = *reinterpret_cast<const uint32_t*>(&b);
+                    for (int j = 0; j < 16; j++) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[2 * j]) * inv_l,
+                                                                       __uint_as_float(r[2 * j + 1]) * inv_l);
+                        x[16 * h + j] = *reinterpret_cast<const uint32_t*>(&b);
                     }
-                    dst[g] = make_uint4(x[0], x[1], x[2], x[3]);
                 }
+                store_rows(stage, x, dst ? dst + 128 * c : nullptr);
             }
         }
         // O read before the next unit's first product overwrites it
