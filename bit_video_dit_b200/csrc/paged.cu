@@ -665,10 +665,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(co
 
 // Short sequences: a unit a CTA, its tiles shared out among eight warps that
 // join in shared memory, so that one launch does.  Up to 64 tiles (2048 keys)
-// it is the faster way (1, 8 and 64 sequences of 8 heads of 128: 700 keys 9.1,
-// 9.1, 10.4 us against 13.7, 16.8, 14.5 with runs; 1500 keys 11.3, 14.9, 32.8
-// against 19.4, 18.2, 35.2; 3000 keys 18.6, 26.2, 54.8 against 18.4, 20.8,
-// 55.7), and sequences much shorter than the longest cost it little.
+// it is the faster way (1, 8 and 64 sequences of 8 heads of 128: 700 keys 7.4,
+// 8.8, 18.9 us against 15.3, 18.9, 22.8 with runs; 1500 keys 11.1, 14.9, 32
+// against 14.6, 18.6, 35; 3000 keys 18.0, 26.1, 54.1 against 16.0, 17.9, 54.4),
+// and sequences much shorter than the longest cost it little.
 constexpr int kUnitWarps = 8, kUnitStages = 2;
 constexpr int kUnitTiles = 64;  // the longest sequence (tiles) that takes this way
 template <int D>
