@@ -735,8 +735,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     constexpr int kBatch = COLS == kChunkRows ? 2 : 8;  // (a unit of chunks rarely lies in more than two runs)
     const int4 cut = __ldcg(a.cut + blockIdx.x);
     const int lane = threadIdx.x & 31, n = (int)blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (cut.x == 0 || n >= cut.w) return;
-    const int first = __ldg(v.row_start + cut.y / a.row_tiles);  // (the worker has checked it)
+    // (a record or row range that something else has overwritten meanwhile must not lead outside the tensors)
+    if (cut.x <= 0 || cut.x > (int)(gridDim.x - blockIdx.x) || n >= min(cut.w, COLS)) return;
+    const int b = cut.y / a.row_tiles;
+    if ((unsigned)b >= (unsigned)v.n_seqs || (unsigned)cut.z >= (unsigned)v.kv_heads) return;
+    const int first = __ldg(v.row_start + b);
     // piece 0 is the end of this worker's run, piece p the beginning of the p-th later one's
     auto at = [&](int p) { return (int64_t)(2 * ((int)blockIdx.x + p) + (p == 0)) * COLS + n; };
     float mx = kFloor, sum = 0.0f, y[D / 32];
@@ -782,7 +785,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     }
     const float f2 = sum == 0.0f ? 0.0f : __fdiv_rn(__ldg(v.a32[1]), sum);
     const int f = cut.y % a.row_tiles * COLS + n;
-    const int64_t row = first + f / a.group, qh = cut.z * a.group + f % a.group;
+    const int64_t row = (int64_t)first + f / a.group, qh = (int64_t)cut.z * a.group + f % a.group;
+    if (row < 0 || row >= v.n_rows) return;
     __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + (row * a.ld_o + qh * D) * 2);
 #pragma unroll
     for (int e = 0; e < D / 64; e++) dst[32 * e + lane] = __floats2bfloat162_rn(y[2 * e] * f2, y[2 * e + 1] * f2);

@@ -164,7 +164,8 @@ struct Piece {
 
 struct Run {
     int64_t x, end, base;  // the run's next tile and end, first tile of the pair
-    int worker, pair, per;
+    int64_t per;           // tiles of every run but the last
+    int worker, pair;
 };
 
 // What beginning and ending a unit costs, in tiles: a unit counts as that many
@@ -228,8 +229,8 @@ __device__ __forceinline__ Run make_run(const AttnArgs& a, int worker, int least
     const long long workers = (long long)gridDim.x * WORKERS;
     Run run;
     run.worker = (int)blockIdx.x * WORKERS + worker;
-    run.per = (int)max((long long)least, (total + workers - 1) / workers);
-    run.x = (int64_t)run.worker * run.per;
+    run.per = max((long long)least, (total + workers - 1) / workers);
+    run.x = run.worker * run.per;
     run.end = min((int64_t)total, run.x + run.per);
     run.pair = pairs;
     run.base = 0;
@@ -273,7 +274,7 @@ __device__ __forceinline__ bool next_piece(const AttnArgs& a, Run& run, Piece& p
             p.slot = 2 * run.worker;
         } else if (p.end < real) {
             p.slot = 2 * run.worker + 1;
-            p.pieces = 1 + (real - p.end + run.per - 1) / run.per;
+            p.pieces = (int)(1 + (real - p.end + run.per - 1) / run.per);
         } else {
             p.slot = -1;
         }
