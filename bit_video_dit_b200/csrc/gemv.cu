@@ -27,8 +27,8 @@
 // through the ring before its pieces and have a power of their own, which comes
 // off the chunk's sums.
 //
-// Measured: 28672 x 8192 (132 MB) 32 us with one row (4.1 TB/s), 40 with 8, 51
-// with 16; 14336 x 4096 12.6, 14, 19.  What bounds it is the conversion and
+// Measured: 28672 x 8192 (132 MB) 31 us with one row (4.2 TB/s), 40 with 8, 49
+// with 16; 14336 x 4096 12.5, 14, 18.  What bounds it is the conversion and
 // integer pipe, with the issue slots half full: decoding a pair of codes takes
 // 3.6 cycles of a scheduler, which alone is 14 us of that weight, and scaling the
 // activations, addresses and scale bytes the rest; hence few, large passes.
@@ -92,13 +92,13 @@ __device__ __forceinline__ uint4 lds16(uint32_t p) {
     return v;
 }
 
-// What a CTA computes: `whole` quads from quad0 on, then the groups [g0, g1),
-// its share of those that whole quads for every CTA leave over.  (Groups dealt
-// out without regard to the quads: a CTA's 12 lay in four of them, and a piece's
-// overhead is per quad.)
+// What a CTA computes: `whole` quads from quad0 on, then the groups [g0, g1) of
+// those that whole quads for every CTA leave over: one, an aligned pair or a
+// quad, so that they lie in one quad (a piece's overhead is per quad; dealt out
+// evenly, two groups of 4096 x 4096 lay in two: 8.1 us a product, 6.4 so).
 struct Share {
     int quad0, whole, g0, g1;
-    __device__ __forceinline__ int count() const { return whole + (g1 > g0 ? (g1 - 1) / 4 - g0 / 4 + 1 : 0); }
+    __device__ __forceinline__ int count() const { return whole + (g1 > g0 ? 1 : 0); }
 };
 
 // The CTA's q-th quad: of its rows 16 i + r, i in [lo, hi) belong to the CTA and
@@ -107,10 +107,10 @@ struct Quad {
     int row0, lo, hi;
     __device__ __forceinline__ Quad(const Share& s, int i) {
         const bool full = i < s.whole;
-        const int q = full ? s.quad0 + i : s.g0 / 4 + i - s.whole;
+        const int q = full ? s.quad0 + i : s.g0 / 4;
         row0 = (q >> 1) * 128 + (q & 1) * 16;
-        lo = full ? 0 : max(0, s.g0 - 4 * q);
-        hi = full ? 4 : min(4, s.g1 - 4 * q);
+        lo = full ? 0 : s.g0 & 3;
+        hi = full ? 4 : lo + s.g1 - s.g0;
     }
 };
 
@@ -192,8 +192,9 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) gemv_kernel(const __grid
     share.whole = a.groups / 4 / (int)gridDim.x;
     share.quad0 = share.whole * (int)blockIdx.x;
     const int spread = share.whole * (int)gridDim.x * 4, rest = a.groups - spread;  // rest < 4 gridDim.x
-    share.g0 = spread + rest * (int)blockIdx.x / (int)gridDim.x;
-    share.g1 = spread + rest * ((int)blockIdx.x + 1) / (int)gridDim.x;
+    const int each = rest <= (int)gridDim.x ? 1 : rest <= 2 * (int)gridDim.x ? 2 : 4;
+    share.g0 = min(a.groups, spread + each * (int)blockIdx.x);
+    share.g1 = min(a.groups, share.g0 + each);
     const int quads = share.count();
     if (quads == 0) return;
 
