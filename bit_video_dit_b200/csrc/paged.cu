@@ -668,7 +668,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_kernel(co
 // it is the faster way (1, 8 and 64 sequences of 8 heads of 128: 700 keys 7.4,
 // 8.8, 18.9 us against 15.3, 18.9, 22.8 with runs; 1500 keys 11.1, 14.9, 32
 // against 14.6, 18.6, 35; 3000 keys 18.0, 26.1, 54.1 against 16.0, 17.9, 54.4),
-// and sequences much shorter than the longest cost it little.
+// and sequences much shorter than the longest cost it little.  Longer ones take it
+// too where a window makes their spans alike and the units fill one wave of CTAs
+// to three quarters or more (windows of 4096 of 8 heads, 128 and 64 wide: 32
+// sequences 39 and 25 us against 45 and 30 with runs; 24: 38.5 and 24.8 against
+// 36.1 and 25.5; 48, which need two waves: 58 and 40 against 57 and 41).
 constexpr int kUnitWarps = 8, kUnitStages = 2;
 constexpr int kUnitTiles = 64;  // the longest sequence (tiles) that takes this way
 template <int D>
@@ -932,7 +936,9 @@ bool make_plan(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, int heads,
     const int64_t tiles = (seen / keys + 3) * p->row_tiles * std::max(1, r->n_seqs);  // ragged at both ends and the sinks'
     p->ctas = (int)std::min<int64_t>(p->ctas, (tiles * c->kv_heads + least - 1) / least);
     const int64_t units = (int64_t)p->row_tiles * std::max(1, r->n_seqs) * c->kv_heads;
-    p->units = !p->chunks && seen / keys < kUnitTiles && units < ((int64_t)1 << 31);
+    const int64_t wave = kSms * (p->cols == 8 ? 2 : 1);
+    const bool alike = seen < r->max_len && units <= wave && 4 * units >= 3 * wave;
+    p->units = !p->chunks && (seen / keys < kUnitTiles || alike) && units < ((int64_t)1 << 31);
     if (p->units) {
         p->ctas = (int)units;
         p->workers = 0;

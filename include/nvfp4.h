@@ -479,7 +479,8 @@ nvfp4_status nvfp4_paged_gather(const nvfp4_paged_cache* cache, const nvfp4_page
  * NVFP4_ERR_TIMEOUT (info = which wait) and leaves o incomplete.  Both deal the
  * key tiles out in equal runs, whatever the lengths, and a second launch joins
  * the rows whose keys lie in several runs; decode steps whose spans (max_len, or
- * window and sinks) are below 2048 keys take one launch.  max_rows decides for
+ * window and sinks) are below 2048 keys, or windows that fill the GPU evenly,
+ * take one launch.  max_rows decides for
  * all sequences of a call: decode steps among long chunks run faster in a call
  * of their own. */
 size_t nvfp4_paged_attention_workspace_bytes(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows,

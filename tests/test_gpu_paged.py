@@ -449,6 +449,17 @@ def test_long_decode_steps(d, page, counts, heads, window, sinks):
     _attend(s, heads, window=window, sinks=sinks, seed=heads)
 
 
+@pytest.mark.parametrize("heads,n", [(4, 230), (4, 296), (4, 297), (12, 120), (12, 149)])
+def test_windows_of_many_sequences(heads, n):
+    """Numbers of sequences around those at which long windows change their way of being shared out."""
+    require_gpu()
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.integers(1, 30, n)]
+    lens[3], lens[n - 1] = 2300, 2111
+    s = Setup(lens, [1] * n, 1, 64, 32, seed=n).fill()
+    _attend(s, heads, window=2100, sinks=5, seed=heads)
+
+
 @pytest.mark.parametrize("count", [1, 2])
 @pytest.mark.parametrize("max_len", [0, 40])
 def test_lengths_beyond_the_hosts_bound(count, max_len):
