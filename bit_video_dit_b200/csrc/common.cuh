@@ -216,6 +216,15 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
                  : "memory");
 }
 
+// A load in a kernel that is launched programmatically (it is resident before the
+// kernel ahead of it has ended, and reads only behind griddepcontrol.wait).  Not
+// __ldg: the read-only path wants data that nobody writes while the grid lives,
+// and the kernel ahead may still be writing it.
+template <class T>
+__device__ __forceinline__ T ld_coherent(const T* p) {
+    return *p;
+}
+
 // Streaming 16-byte load (read once, do not keep in L1).
 __device__ __forceinline__ uint4 ld_stream16(const void* p) {
     uint4 v;

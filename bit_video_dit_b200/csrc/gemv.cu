@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) gemv_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < kParts; i++) {
             const int p = warp + i * kWarps, m = p / row_parts, j = (p - m * row_parts) * 32 + lane;
-            v[i] = p < parts && j < a.k / 8 ? __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)m * a.ldx * 2) + j)
+            v[i] = p < parts && j < a.k / 8 ? ld_coherent(reinterpret_cast<const uint4*>(a.x + (int64_t)m * a.ldx * 2) + j)
                                             : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) gemv_kernel(const __grid
         __syncthreads();
     }
 
-    const float alpha = __ldg(a.a32);
+    const float alpha = ld_coherent(a.a32);
     int slot = 0;
     auto next_piece = [&]() {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");

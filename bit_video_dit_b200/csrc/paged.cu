@@ -47,13 +47,14 @@ struct RowArgs {
 // bytes each leave half a sector to the other instruction).
 __device__ __forceinline__ void load32(const uint8_t* p, bool wide, uint4* x) {
     if (wide) {
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(x[0].x), "=r"(x[0].y), "=r"(x[0].z), "=r"(x[0].w), "=r"(x[1].x), "=r"(x[1].y), "=r"(x[1].z),
                        "=r"(x[1].w)
-                     : "l"(p));
+                     : "l"(p)
+                     : "memory");
     } else {
-        x[0] = __ldg(reinterpret_cast<const uint4*>(p));
-        x[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+        x[0] = ld_coherent(reinterpret_cast<const uint4*>(p));
+        x[1] = ld_coherent(reinterpret_cast<const uint4*>(p) + 1);
     }
 }
 __device__ __forceinline__ void store32(uint8_t* p, bool wide, const uint32_t* o) {
@@ -74,7 +75,7 @@ __device__ __forceinline__ int find_seq(const View& v, int row, int lane) {
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
         const int64_t i = lo + (int64_t)lane * step;
-        const bool le = lane == 0 || (i < hi && __ldg(v.row_start + i) <= row);
+        const bool le = lane == 0 || (i < hi && ld_coherent(v.row_start + i) <= row);
         lo += (__popc(__ballot_sync(0xFFFFFFFFu, le)) - 1) * step;
         hi = min(hi, lo + step);
     }
@@ -88,7 +89,8 @@ struct RowBlock {
 
 // 16 elements (K with RoPE when tables are given, as nvfp4_kv_append_rope) to
 // codes and scale at cache row `at`, block `blk`.
-__device__ __forceinline__ void append_block(const RowArgs& a, const RowBlock& r, int t, int row, int blk, uint32_t at) {
+__device__ __forceinline__ void append_block(const RowArgs& a, const RowBlock& r, int t, float a32, int row, int blk,
+                                             uint32_t at) {
     const View& v = a.v;
     float x[16];
     bf16x8_to_f32(r.x[0], x);
@@ -99,7 +101,7 @@ __device__ __forceinline__ void append_block(const RowArgs& a, const RowBlock& r
         const float4* ps = reinterpret_cast<const float4*>(a.rope_sin + off);
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            const float4 c4 = __ldg(pc + i), s4 = __ldg(ps + i);
+            const float4 c4 = ld_coherent(pc + i), s4 = ld_coherent(ps + i);
             const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
             for (int e = 0; e < 4; e++) {
@@ -110,15 +112,14 @@ __device__ __forceinline__ void append_block(const RowArgs& a, const RowBlock& r
             }
         }
     }
-    const BlockScale b = block_scale(fmaxf(absmax8(x), absmax8(x + 8)), __ldg(v.a32[t]));
+    const BlockScale b = block_scale(fmaxf(absmax8(x), absmax8(x + 8)), a32);
     uint8_t* codes = const_cast<uint8_t*>(v.codes[t]) + (uint64_t)at * (v.d / 2) + 8 * blk;
     *reinterpret_cast<uint2*>(codes) = make_uint2(encode8(x, b.inv), encode8(x + 8, b.inv));
     const_cast<uint8_t*>(v.scales[t])[(uint64_t)at * (v.d / 16) + blk] = (uint8_t)b.code;
 }
 
-__device__ __forceinline__ void gather_block(const RowArgs& a, const RowBlock& r, int t, uint8_t* dst) {
+__device__ __forceinline__ void gather_block(const RowArgs& a, const RowBlock& r, float a32, uint8_t* dst) {
     const __half2 s2 = e4m3x2_to_half2((uint16_t)(r.x[0].z | (r.x[0].z << 8)));
-    const float a32 = __ldg(a.v.a32[t]);
     uint32_t h[8], o[8];
     decode8(r.x[0].x, s2, h);
     decode8(r.x[0].y, s2, h + 4);
@@ -145,14 +146,14 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3) rows_kernel(const __grid_co
     if (r0 >= v.n_rows) return;
     const int last = (int)min((int64_t)v.n_rows, r0 + per) - 1;
     int b = find_seq(v, (int)r0, lane);
-    const int b1 = __ldg(v.row_start + b + 1) > last ? b : find_seq(v, last, lane);
+    const int b1 = ld_coherent(v.row_start + b + 1) > last ? b : find_seq(v, last, lane);
     const int row = (int)r0 + lane / blocks, blk = lane % blocks;
     if (row > last) return;
     if (b != b1) {  // the rows' own sequences lie between
         int lo = b, hi = b1 + 1;
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (__ldg(v.row_start + mid) <= row) lo = mid;
+            if (ld_coherent(v.row_start + mid) <= row) lo = mid;
             else hi = mid;
         }
         b = lo;
@@ -167,6 +168,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3) rows_kernel(const __grid_co
     // the cache's row of head 0, and a head's distance from the one before it (rows below 2^32: host)
     const int off = none ? 0 : v.page_shift >= 0 ? pos & (v.page_size - 1) : pos % v.page_size;
     const uint32_t at0 = (uint32_t)page * (uint32_t)v.kv_heads * (uint32_t)v.page_size + (uint32_t)off;
+    // (read once: behind the stores below the compiler would have to read them again)
+    const float a32[2] = {ld_coherent(v.a32[0]), ld_coherent(v.a32[1])};
     const int i0 = (int)((int64_t)a.items * part / a.parts), i1 = (int)((int64_t)a.items * (part + 1) / a.parts);
     for (int i = i0; i < i1; i += kInFlight) {
         RowBlock r[kInFlight];
@@ -181,8 +184,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3) rows_kernel(const __grid_co
             } else if (none) {
                 r[u].x[0] = make_uint4(0u, 0u, 0u, 0u);
             } else {
-                const uint2 c = __ldg(reinterpret_cast<const uint2*>(v.codes[t] + (uint64_t)at * (v.d / 2) + 8 * blk));
-                r[u].x[0] = make_uint4(c.x, c.y, __ldg(v.scales[t] + (uint64_t)at * (v.d / 16) + blk), 0u);
+                const uint2 c = ld_coherent(reinterpret_cast<const uint2*>(v.codes[t] + (uint64_t)at * (v.d / 2) + 8 * blk));
+                r[u].x[0] = make_uint4(c.x, c.y, ld_coherent(v.scales[t] + (uint64_t)at * (v.d / 16) + blk), 0u);
             }
         }
 #pragma unroll
@@ -190,9 +193,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3) rows_kernel(const __grid_co
             const int head = (i + u) >> 1, t = (i + u) & 1;
             if (i + u >= i1) break;
             if (APPEND)
-                append_block(a, r[u], t, row, blk, at0 + (uint32_t)head * (uint32_t)v.page_size);
+                append_block(a, r[u], t, t ? a32[1] : a32[0], row, blk, at0 + (uint32_t)head * (uint32_t)v.page_size);
             else
-                gather_block(a, r[u], t, a.rows[t] + ((int64_t)row * a.ld[t] + (int64_t)head * v.d + 16 * blk) * 2);
+                gather_block(a, r[u], t ? a32[1] : a32[0],
+                             a.rows[t] + ((int64_t)row * a.ld[t] + (int64_t)head * v.d + 16 * blk) * 2);
         }
     }
 }
@@ -388,7 +392,7 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
         const uint4* src = reinterpret_cast<const uint4*>(
             a.q + ((int64_t)(s.first + f / a.group) * a.ld_q + (int64_t)(head * a.group + f % a.group) * D + D / 4 * t) * 2);
 #pragma unroll
-        for (int i = 0; i < D / 32; i++) raw[j][i] = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < D / 32; i++) raw[j][i] = in ? ld_coherent(src + i) : make_uint4(0u, 0u, 0u, 0u);
     }
 
     // Copies run kStages - 1 tiles ahead.  A tile whose 32 keys are all seen by some row and
@@ -438,7 +442,7 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
     float c_col[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; j++) {
-        const float down = scale_row<D / 32>(raw[j], qb[j]) * (__ldg(v.a32[0]) * a.scale_log2);
+        const float down = scale_row<D / 32>(raw[j], qb[j]) * (ld_coherent(v.a32[0]) * a.scale_log2);
 #pragma unroll
         for (int e = 0; e < 2; e++) c_col[j][e] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4 * e);
     }
@@ -596,7 +600,7 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
     }
     __syncwarp();  // every lane has left the ring (its copies are done: none was begun behind the last tile)
 
-    const float back = __ldg(v.a32[1]);
+    const float back = ld_coherent(v.a32[1]);
 #pragma unroll
     for (int j = 0; j < NT; j++)
 #pragma unroll
@@ -704,7 +708,7 @@ __global__ void __launch_bounds__(kUnitWarps * 32, NT == 1 ? 2 : 1) unit_kernel(
     decode_piece<D, NT, kUnitStages>(a, u, smem_u32(ring_mem) + (uint32_t)(warp * kBytes), part,
                                      reinterpret_cast<float2*>(part + kCols * D));
     __syncthreads();
-    const float back = __ldg(v.a32[1]);
+    const float back = ld_coherent(v.a32[1]);
     for (int i = threadIdx.x; i < u.rows.n * (D / 2); i += kUnitWarps * 32) {
         const int n = i / (D / 2), d = i % (D / 2) * 2;
         float mx = kFloor, sum = 0.0f, y0 = 0.0f, y1 = 0.0f;
@@ -743,7 +747,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     if (cut.x <= 0 || cut.x > (int)(gridDim.x - blockIdx.x) || n >= min(cut.w, COLS)) return;
     const int b = cut.y / a.row_tiles;
     if ((unsigned)b >= (unsigned)v.n_seqs || (unsigned)cut.z >= (unsigned)v.kv_heads) return;
-    const int first = __ldg(v.row_start + b);
+    const int first = ld_coherent(v.row_start + b);
     // piece 0 is the end of this worker's run, piece p the beginning of the p-th later one's
     auto at = [&](int p) { return (int64_t)(2 * ((int)blockIdx.x + p) + (p == 0)) * COLS + n; };
     float mx = kFloor, sum = 0.0f, y[D / 32];
@@ -787,7 +791,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
             }
         }
     }
-    const float f2 = sum == 0.0f ? 0.0f : __fdiv_rn(__ldg(v.a32[1]), sum);
+    const float f2 = sum == 0.0f ? 0.0f : __fdiv_rn(ld_coherent(v.a32[1]), sum);
     const int f = cut.y % a.row_tiles * COLS + n;
     const int64_t row = (int64_t)first + f / a.group, qh = (int64_t)cut.z * a.group + f % a.group;
     if (row < 0 || row >= v.n_rows) return;

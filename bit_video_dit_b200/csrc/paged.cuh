@@ -35,10 +35,10 @@ struct Seq {
 // the arrays hold, a launch's work is bounded and no position overflows.
 __device__ __forceinline__ Seq load_seq(const View& v, int b) {
     Seq s;
-    const int r0 = __ldg(v.row_start + b), r1 = __ldg(v.row_start + b + 1);
+    const int r0 = ld_coherent(v.row_start + b), r1 = ld_coherent(v.row_start + b + 1);
     s.first = r0;
     s.n = r1 - r0;
-    s.len = __ldg(v.lens + b);
+    s.len = ld_coherent(v.lens + b);
     if (r0 < 0 || r1 < r0 || r1 > v.n_rows || s.len < 0 || s.len > v.room) {
         record_error(v.err, NVFP4_ERR_DEVICE, (uint32_t)b);
         s.n = 0;
@@ -50,7 +50,7 @@ __device__ __forceinline__ Seq load_seq(const View& v, int b) {
 // The page that holds position pos < len of sequence b, or -1 (reported, info =
 // b) when the table does not list one of the cache's pages for it.
 __device__ __forceinline__ int page_of(const View& v, int b, int pos) {
-    const int p = __ldg(v.pages + (int64_t)b * v.max_pages + pos / v.page_size);
+    const int p = ld_coherent(v.pages + (int64_t)b * v.max_pages + pos / v.page_size);
     if (p >= 0 && p < v.n_pages) return p;
     record_error(v.err, NVFP4_ERR_DEVICE, (uint32_t)b);
     return -1;
@@ -59,7 +59,7 @@ __device__ __forceinline__ int page_of(const View& v, int b, int pos) {
 // Entry i of a sequence's page table for the attention, in which -1 stands for
 // a page that is not needed: an entry below 0 becomes -2.
 __device__ __forceinline__ int listed(const int32_t* table, int i) {
-    const int p = __ldg(table + i);
+    const int p = ld_coherent(table + i);
     return p < 0 ? -2 : p;
 }
 

@@ -642,6 +642,7 @@ nvfp4_status launch(const AttnArgs& a, unsigned ctas, cudaStream_t stream) {
         return at.numRegs == kLaunchRegs ? NVFP4_OK : NVFP4_ERR_UNSUPPORTED;
     });
     if (st != NVFP4_OK) return st;
+    // (no programmatic launch: the kernel ahead has ended, so the read-only loads above are sound)
     chunk_kernel<D><<<ctas, kThreads, Smem<D>::bytes, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
