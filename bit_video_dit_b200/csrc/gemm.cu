@@ -414,7 +414,7 @@ __device__ __forceinline__ void load_row32(const __nv_bfloat16* p, int valid, fl
     if (valid >= 32) {
         const uint4* q = reinterpret_cast<const uint4*>(p);
 #pragma unroll
-        for (int i = 0; i < 4; i++) bf16x8_to_f32(__ldg(q + i), out + 8 * i);
+        for (int i = 0; i < 4; i++) bf16x8_to_f32(ld_coherent(q + i), out + 8 * i);
     } else {
 #pragma unroll
         for (int i = 0; i < 32; i++) out[i] = (i < valid) ? __bfloat162float(p[i]) : 0.0f;
@@ -591,8 +591,8 @@ __device__ void epilogue(const Params& p, Smem<Cfg<PAIR>::STAGES>* s, uint32_t t
     const int q = warp & 3;                 // TMEM lane quarter this warp may access
     const int h = (warp - 2) >> 2;          // column chunks h, h + 2, h + 4, h + 6
     const int et = (warp - 2) * 32 + lane;  // 0..255 over the epilogue warps
-    const float alpha = __fmul_rn(__ldg(p.ga), __ldg(p.gb));
-    const float oa32 = p.out_codes ? __ldg(p.out_gscale) : 0.0f;
+    const float alpha = __fmul_rn(ld_coherent(p.ga), ld_coherent(p.gb));
+    const float oa32 = p.out_codes ? ld_coherent(p.out_gscale) : 0.0f;
     // the requant's reciprocal table: one entry per epilogue thread (256 codes)
     if (p.out_codes) {
         const float sv = e4m3_value((uint32_t)et);

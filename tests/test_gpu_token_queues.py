@@ -72,3 +72,31 @@ def test_decoder_layers_in_one_queue(counts, lens):
 
     for a, b in zip(layers(True), layers(False)):
         assert torch.all(torch.isfinite(a)) and torch.equal(a, b)
+
+
+def test_a_gemm_behind_the_kernel_that_writes_its_residual():
+    """nvfp4_gemm with CTA pairs right behind the nvfp4_gemv that writes rows of its residual, and behind the nvfp4_gemm
+    whose result is its residual: the same bits as with every call waited for."""
+    require_gpu()
+    m, n, k = 272, 4096, 512
+    w = nv.quantize(dev_bf16(syn.normal_bf16((n, k), seed=1, std=0.06)))
+    a = nv.quantize(dev_bf16(syn.normal_bf16((m, k), seed=2)))
+    x = [dev_bf16(syn.normal_bf16((16, k), seed=10 + i)) for i in range(6)]
+    ws = nv.workspace(nv.OP_GEMM, m, n, k)
+
+    def queue(wait):
+        y = torch.zeros((m, n), dtype=torch.bfloat16, device="cuda")
+        out = [torch.empty_like(y) for _ in range(2 * len(x))]
+        torch.cuda.synchronize()
+        for i, t in enumerate(x):
+            at = slice(16 * i, 16 * i + 16) if i % 2 else slice(m - 16 * i - 16, m - 16 * i)
+            for call in (lambda: nv.gemv(t, w, out=y[at]), lambda: nv.gemm(a, w, out=out[2 * i], residual=y, ws=ws),
+                         lambda: nv.gemm(a, w, out=out[2 * i + 1], residual=out[2 * i], ws=ws)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        assert nv.read_device_error(ws) == (nv.OK, 0)
+        return out
+
+    for p, q in zip(queue(True), queue(False)):
+        assert torch.all(torch.isfinite(p)) and torch.equal(p, q)
