@@ -451,8 +451,9 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
     const int all_lo = a.window > 0 ? s.len - s.n + (f0 + rows.n - 1) / a.group - a.window + 1 : 0;
     const int all_sink = a.sinks - kKeys;
 
-    // a column's reference maximum m as -m, and what an exponent relative to it must exceed for m to move; before
+    // a column's reference m (paged.cuh) as -m, and what an exponent relative to it must exceed for m to move; before
     // its first visible key m is 0 and any exponent does
+    constexpr float kLimit = kLazy + kHead;
     float nm[NT][2], limit[NT][2], l[NT][2], o[NT][kSteps][4];
 #pragma unroll
     for (int j = 0; j < NT; j++) {
@@ -546,8 +547,9 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
                     if (mx > limit[j][e]) {
-                        const float f = limit[j][e] == kLazy ? ex2(-mx) : 0.0f;
-                        limit[j][e] = kLazy;
+                        mx -= kHead;
+                        const float f = limit[j][e] == kLimit ? ex2(-mx) : 0.0f;
+                        limit[j][e] = kLimit;
                         nm[j][e] -= mx;
                         l[j][e] *= f;
 #pragma unroll
@@ -574,7 +576,8 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
                     p[e] = ex2(z[q][j][e]);
                     l[j][e & 1] += p[e];
                 }
-                // the weights go to the tensor cores in binary16 (2^-11 of each)
+                // the weights go to the tensor cores in binary16 (2^-11 of each, 2^-32 of the row's largest: paged.cuh),
+                // an eighth of what the result's store in bf16 rounds; binary32 would need a second product of the rest
                 pb[j][0] = transpose8x8(h2_bits(__floats2half2_rn(p[0], p[1])));
                 pb[j][1] = transpose8x8(h2_bits(__floats2half2_rn(p[2], p[3])));
             }
@@ -616,7 +619,7 @@ __device__ __forceinline__ void decode_piece(const AttnArgs& a, const Piece& u, 
 #pragma unroll
                 for (int r = 0; r < kSteps; r += 2)
                     dst[r / 2] = make_float4(o[j][r][e], o[j][r][e + 2], o[j][r + 1][e], o[j][r + 1][e + 2]);
-                if (g == 0) part_ml[at] = make_float2(limit[j][e] == kLazy ? -nm[j][e] : kFloor, sum);
+                if (g == 0) part_ml[at] = make_float2(limit[j][e] == kLimit ? -nm[j][e] : kFloor, sum);
             } else {
                 const float f = sum == 0.0f ? 0.0f : __fdiv_rn(back, sum);  // a row that sees no key: zeros
                 const int row = s.first + (f0 + n) / a.group, qh = head * a.group + (f0 + n) % a.group;

@@ -112,7 +112,14 @@ constexpr int kChunkLeast = 3;   // tiles of a run (16 rows over 1000 keys: 17.3
 struct AttnArgs;
 nvfp4_status launch_chunks(const AttnArgs& a, unsigned ctas, cudaStream_t stream);
 
-constexpr float kLazy = 8.0f;     // a reference maximum moves when exceeded by more than 2^8
+// A row's weights are taken relative to a reference that is set kHead binary
+// orders below the largest score so far and moves when that is exceeded by more
+// than kLazy orders (decode; chunks: when a tile's weights sum above 2^15).  So
+// the weights reach 2^15 at most, which binary16 holds, and keep its 11 bits down
+// to 2^-21 of the largest and 2^-32 of it below: with the reference at the
+// largest score itself, thousands of keys 24 to 26 orders below an attention
+// sink lost their part of the result or doubled it.
+constexpr float kLazy = 8.0f, kHead = 7.0f;
 constexpr float kFloor = -1e30f;  // the reference before any visible key
 
 struct AttnArgs {

@@ -28,9 +28,9 @@
 // Measured and not taken: 16 softmax warps (each half a tile's columns; 1024
 // us), four issuing threads (752), a lane waiting for its warp (820), an eighth
 // of the exponentials as polynomials (747).
-// The softmax takes one pass a tile against a reference maximum that moves
-// only when a row's weights in the tile sum above 2^15 (binary16 holds those
-// below).  Every wait is bounded; a timeout records NVFP4_ERR_TIMEOUT and every
+// The softmax takes one pass a tile against a reference 7 binary orders below the
+// largest score (paged.cuh) that moves only when a row's weights in the tile sum
+// above 2^15 (binary16 holds those below).  Every wait is bounded; a timeout records NVFP4_ERR_TIMEOUT and every
 // role stops.
 #include <algorithm>
 #include <cmath>
@@ -396,10 +396,11 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& a, Shared& sh, uint
                 // tcgen05.ld / st are warp-collective: the whole warp takes part
                 const float mt = (all ? tile_max<false>(t_s, rm) : tile_max<true>(t_s, rm)) * c_s;  // c_s >= 0
                 float factor = 1.0f;
+                // (a sum above 2^15 means a score more than 9 above m; m 7 below the largest brings it to 2^13 at most)
                 if (redo && mt - m > kLazy) {
-                    factor = ex2(m - mt);  // 0 on the first tile (m = -inf)
+                    factor = ex2(m - (mt - kHead));  // 0 on the first tile (m = -inf)
                     l *= factor;
-                    m = mt;
+                    m = mt - kHead;
                 }
                 if (!first && __any_sync(0xFFFFFFFFu, factor != 1.0f)) {
                     // the last tile's product may still be adding to O

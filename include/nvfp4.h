@@ -468,7 +468,8 @@ nvfp4_status nvfp4_paged_gather(const nvfp4_paged_cache* cache, const nvfp4_page
  * h / (heads / kv_heads).  scale 0: 1 / sqrt(head_dim).  Keys and values are
  * the exact e2m1 * s * a32; queries are scaled by a power of two to binary16;
  * binary32 accumulation and softmax; the weights go to the second product in
- * binary16.  A row that sees no key gives zeros.  Pages that hold no visible
+ * binary16 (2^-11 of each, and 2^-32 of the row's largest for those below 2^-21
+ * of it).  A row that sees no key gives zeros.  Pages that hold no visible
  * key are not looked up, so a window's caller may have given them back; places
  * that no row sees may hold any bytes.  A NaN query gives NaN, in its row alone.
  * workspace: nvfp4_paged_attention_workspace_bytes of the same arguments (0:
