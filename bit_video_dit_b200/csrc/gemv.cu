@@ -406,7 +406,6 @@ extern "C" nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t m, int64_t ldx, c
     const int64_t n = W->rows, k = W->cols;
     if (k % 64 != 0 || n > (1 << 30) || k > (1 << 30) || m > gemv::kMaxM) return NVFP4_ERR_UNSUPPORTED;
     float* y32 = ep ? ep->debug_y : nullptr;
-    if (!y_bf16 && !y32) return NVFP4_ERR_INVALID_ARG;
     if (ldx < k || (y_bf16 && ldy < n)) return NVFP4_ERR_INVALID_ARG;
     if (ep) {
         if (ep->act != NVFP4_ACT_NONE && ep->act != NVFP4_ACT_GELU_TANH) return NVFP4_ERR_INVALID_ARG;
@@ -415,8 +414,8 @@ extern "C" nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t m, int64_t ldx, c
         if (ep->out_codes || ep->out_scales || ep->out_global_scale || ep->out_amax || ep->out_col0 || ep->out_cols)
             return NVFP4_ERR_UNSUPPORTED;
     }
-    if (m == 0) return NVFP4_OK;
-    if (!x_bf16) return NVFP4_ERR_INVALID_ARG;
+    if (m == 0) return NVFP4_OK;  // (before the row tensors: an empty one has no address)
+    if (!x_bf16 || (!y_bf16 && !y32)) return NVFP4_ERR_INVALID_ARG;
     auto odd = [](const void* p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; };
     if (odd(x_bf16, 15u) || ldx % 8 != 0 || odd(W->codes, 15u) || odd(W->scales, 15u) || odd(W->global_scale, 3u) ||
         odd(y_bf16, 1u) || odd(y32, 3u))
