@@ -861,7 +861,7 @@ nvfp4_status check_paged(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, 
     return NVFP4_OK;
 }
 
-View make_view(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, void* ws) {
+View make_view(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, void* record) {
     View v{};
     v.codes[0] = static_cast<const uint8_t*>(c->k_codes);
     v.codes[1] = static_cast<const uint8_t*>(c->v_codes);
@@ -883,7 +883,7 @@ View make_view(const nvfp4_paged_cache* c, const nvfp4_paged_rows* r, void* ws) 
     v.max_pages = r->max_pages;
     v.n_rows = r->n_rows;
     v.room = (int)std::min<int64_t>((int64_t)r->max_pages * c->page_size, 1 << 30);
-    v.err = static_cast<DevError*>(ws);
+    v.err = static_cast<DevError*>(record);
     return v;
 }
 
@@ -993,10 +993,21 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, co
                                               const void* q_bf16, int64_t ld_q, int32_t heads, int32_t window,
                                               int32_t sinks, float scale, void* o_bf16, int64_t ld_o, void* workspace,
                                               size_t ws_bytes, nvfp4_stream_t stream) {
+    return nvfp4_paged_attention_recorded(cache, rows, q_bf16, ld_q, heads, window, sinks, scale, o_bf16, ld_o, workspace,
+                                          ws_bytes, workspace, stream);
+}
+
+extern "C" nvfp4_status nvfp4_paged_attention_recorded(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows,
+                                                       const void* q_bf16, int64_t ld_q, int32_t heads, int32_t window,
+                                                       int32_t sinks, float scale, void* o_bf16, int64_t ld_o,
+                                                       void* workspace, size_t ws_bytes, void* record,
+                                                       nvfp4_stream_t stream) {
     nvfp4_status st = check_paged(cache, rows, workspace, ws_bytes, kControl);
     if (st != NVFP4_OK) return st;
     st = check_heads(cache, heads, window, sinks);
     if (st != NVFP4_OK) return st;
+    if (!record) return NVFP4_ERR_INVALID_ARG;
+    if (odd(record, 255u)) return NVFP4_ERR_MISALIGNED;
     const int64_t width = (int64_t)heads * cache->head_dim;
     if (!(scale >= 0.0f) || std::isinf(scale) || ld_q < width || ld_o < width) return NVFP4_ERR_INVALID_ARG;
     Plan p;
@@ -1006,7 +1017,7 @@ extern "C" nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, co
     if (!q_bf16 || !o_bf16) return NVFP4_ERR_INVALID_ARG;
     if (odd(q_bf16, 15u) || odd(o_bf16, 15u) || ld_q % 8 != 0 || ld_o % 8 != 0) return NVFP4_ERR_MISALIGNED;
     AttnArgs a{};
-    a.v = make_view(cache, rows, workspace);
+    a.v = make_view(cache, rows, record);
     a.q = static_cast<const uint8_t*>(q_bf16);
     a.o = static_cast<uint8_t*>(o_bf16);
     a.ld_q = ld_q;

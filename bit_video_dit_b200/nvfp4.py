@@ -30,7 +30,7 @@ EXPORTS = ("nvfp4_status_string", "nvfp4_version", "nvfp4_codes_bytes", "nvfp4_s
            "nvfp4_kv_append", "nvfp4_kv_dequant", "nvfp4_test_encode", "nvfp4_quantize_noalloc",
            "nvfp4_ln_modulate_quantize", "nvfp4_quantize_2d", "nvfp4_quantize_t", "nvfp4_attention_chunks",
            "nvfp4_kv_attention", "nvfp4_kv_append_rope", "nvfp4_gemv", "nvfp4_paged_append", "nvfp4_paged_gather",
-           "nvfp4_paged_attention", "nvfp4_paged_attention_workspace_bytes")
+           "nvfp4_paged_attention", "nvfp4_paged_attention_recorded", "nvfp4_paged_attention_workspace_bytes")
 
 
 class NVFP4Error(RuntimeError):
@@ -132,6 +132,8 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_paged_gather.restype = st
         L.nvfp4_paged_attention.argtypes = [pc, pr, vp, i64, i32, i32, i32, ctypes.c_float, vp, i64, vp, sz, vp]
         L.nvfp4_paged_attention.restype = st
+        L.nvfp4_paged_attention_recorded.argtypes = [pc, pr, vp, i64, i32, i32, i32, ctypes.c_float, vp, i64, vp, sz, vp, vp]
+        L.nvfp4_paged_attention_recorded.restype = st
         L.nvfp4_paged_attention_workspace_bytes.argtypes = [pc, pr, i32, i32, i32]
         L.nvfp4_paged_attention_workspace_bytes.restype = sz
         _lib = L
@@ -560,7 +562,9 @@ class PagedKVCache:
     """NVFP4 cache of n_pages pages of page_size tokens x kv_heads x head_dim (64 or 128) for sequences that grow by
     tokens: codes [n_pages, kv_heads, page_size, d / 2] and E4M3 scales [.., d / 16] of K and V, under one tensor
     scale each for the whole cache (k_scale, v_scale: numbers or device float32 tensors; amax / 2688 of a
-    calibration).  The caller hands out the pages.  The cache's tensors are its own for its life: fill them in place."""
+    calibration).  The caller hands out the pages.  The cache's tensors are its own for its life: fill them in place.
+    What the kernels find wrong (a bad page or row range, a wait that ran out) is kept in the record of the workspace
+    given to the call, else in the cache's own, which its calls share: read_device_error(cache.ws_rows)."""
 
     def __init__(self, n_pages: int, page_size: int, kv_heads: int, head_dim: int, *, k_scale, v_scale, device="cuda"):
         self.n_pages, self.page_size, self.kv_heads, self.head_dim = n_pages, page_size, kv_heads, head_dim
@@ -637,13 +641,16 @@ class PagedKVCache:
             _check("nvfp4_paged_gather", st)
         return k_out, v_out
 
-    def attention_workspace(self, rows: PagedRows, heads: int, *, window: int = 0, sinks: int = 0) -> torch.Tensor:
-        """A workspace for attention() with these arguments; calls that may run at the same time take one each."""
+    def _attention_memory(self, rows: PagedRows, heads: int, window: int, sinks: int) -> torch.Tensor:
         n = int(lib().nvfp4_paged_attention_workspace_bytes(self._ref, rows._ref, heads, window, sinks))
         if n == 0:
             raise ValueError("nvfp4_paged_attention_workspace_bytes: refused arguments")
-        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        ws[:256].zero_()
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def attention_workspace(self, rows: PagedRows, heads: int, *, window: int = 0, sinks: int = 0) -> torch.Tensor:
+        """A workspace for attention() with these arguments; calls that may run at the same time take one each."""
+        ws = self._attention_memory(rows, heads, window, sinks)
+        ws[:256].zero_()  # its error record
         return ws
 
     def attention(self, rows: PagedRows, q: torch.Tensor, *, window: int = 0, sinks: int = 0, scale: float = 0.0,
@@ -653,14 +660,15 @@ class PagedKVCache:
         if q.dim() != 3:
             raise ValueError("attention takes q [n_rows, heads, head_dim]")
         heads = q.shape[1]
+        record = self.ws_rows if ws is None else ws
         with _allocating_for(stream):
             if out is None:
                 out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            if ws is None:
-                ws = self.attention_workspace(rows, heads, window=window, sinks=sinks)
+            if ws is None:  # for this call alone
+                ws = self._attention_memory(rows, heads, window, sinks)
         ld_q, ld_o = self._row_stride(rows, heads, q), self._row_stride(rows, heads, out)
-        st = _launch_on(self.index, stream, lib().nvfp4_paged_attention, self._ref, rows._ref, q.data_ptr(), ld_q,
-                        heads, window, sinks, scale, out.data_ptr(), ld_o, ws.data_ptr(), ws.numel())
+        st = _launch_on(self.index, stream, lib().nvfp4_paged_attention_recorded, self._ref, rows._ref, q.data_ptr(), ld_q,
+                        heads, window, sinks, scale, out.data_ptr(), ld_o, ws.data_ptr(), ws.numel(), record.data_ptr())
         if st:
             _check("nvfp4_paged_attention", st)
         return out

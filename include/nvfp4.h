@@ -447,8 +447,8 @@ typedef struct {
  * nvfp4_kv_append_rope does.  A row before its sequence's first position
  * (lens[b] < n_b) is not written.  Two rows must not share a place: pages of
  * two sequences may be the same only where neither writes.
- * workspace: nvfp4_workspace_bytes(NVFP4_OP_PAGED_ROWS, 0, 0, 0) bytes.  One
- * launch. */
+ * workspace: nvfp4_workspace_bytes(NVFP4_OP_PAGED_ROWS, 0, 0, 0) bytes, the
+ * error record alone: calls at the same time may share it.  One launch. */
 nvfp4_status nvfp4_paged_append(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows, const void* k_bf16,
                                 int64_t ld_k, const void* v_bf16, int64_t ld_v, const float* rope_cos,
                                 const float* rope_sin, void* workspace, size_t ws_bytes, nvfp4_stream_t stream);
@@ -490,6 +490,15 @@ nvfp4_status nvfp4_paged_attention(const nvfp4_paged_cache* cache, const nvfp4_p
                                    int64_t ld_q, int32_t heads, int32_t window, int32_t sinks, float scale,
                                    void* o_bf16, int64_t ld_o, void* workspace, size_t ws_bytes,
                                    nvfp4_stream_t stream);
+
+/* The same with the device error record apart from the workspace: `record` is
+ * the control block of another workspace (nvfp4_workspace_bytes of
+ * NVFP4_OP_PAGED_ROWS), which any calls may share, at the same time too; the
+ * workspace may then hold anything and need not outlive the call's work. */
+nvfp4_status nvfp4_paged_attention_recorded(const nvfp4_paged_cache* cache, const nvfp4_paged_rows* rows,
+                                            const void* q_bf16, int64_t ld_q, int32_t heads, int32_t window,
+                                            int32_t sinks, float scale, void* o_bf16, int64_t ld_o, void* workspace,
+                                            size_t ws_bytes, void* record, nvfp4_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Training-side operands  [RN-T] "NVFP4 训练的工程细节"                        */

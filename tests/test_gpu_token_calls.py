@@ -22,3 +22,63 @@ def test_gemv_of_no_rows():
     for y in (nv.gemv(x[:0], w), nv.gemv(x[4:], w, bias=bias, act=nv.ACT_GELU_TANH),
               nv.gemv(x[:0], w, residual=torch.zeros((0, 96), dtype=torch.bfloat16, device="cuda"))):
         assert y.shape == (0, 96) and y.dtype == torch.bfloat16
+
+
+def _step(counts, lens, page=16, heads=2, d=64):
+    """A cache whose sequences have pages of their own, written with normal values, and the step's rows."""
+    held = [-(-n // page) for n in lens]
+    table = torch.full((len(lens), max(held) + 1), -1, dtype=torch.int32)
+    for b, n in enumerate(held):
+        table[b, :n] = sum(held[:b]) + torch.arange(n)
+    cache = nv.PagedKVCache(sum(held), page, heads, d, k_scale=0.004, v_scale=0.004)
+
+    def rows(n, table=table):
+        start = torch.tensor([0, *n]).cumsum(0).to(torch.int32)
+        return nv.PagedRows(start.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), table.cuda(), n_rows=sum(n),
+                            max_rows=max(n), max_len=max(lens))
+
+    x = dev_bf16(syn.normal_bf16((sum(lens), heads, d), seed=7))
+    cache.append(rows(lens), x, x)
+    return cache, rows, table
+
+
+@pytest.mark.parametrize("counts,lens", [([1, 1], [40, 60]), ([1, 2], [60, 3000]), ([1, 50], [60, 3000])])
+def test_what_an_attention_without_a_workspace_finds_is_kept(counts, lens):
+    """A bad page shows in the cache's own record, and stays there through later calls until it is read."""
+    require_gpu()
+    cache, rows, table = _step(counts, lens)
+    q = dev_bf16(syn.normal_bf16((sum(counts), 4, 64), seed=3))
+    good = rows(counts)
+    want = cache.attention(good, q)
+    assert nv.read_device_error(cache.ws_rows) == (nv.OK, 0)
+    bad = table.clone()
+    bad[1, 1] = cache.n_pages
+    cache.attention(rows(counts, bad), q)
+    assert torch.equal(cache.attention(good, q), want)
+    assert nv.read_device_error(cache.ws_rows) == (nv.ERR_DEVICE, 1)
+    assert nv.read_device_error(cache.ws_rows) == (nv.OK, 0)
+    # a workspace that is given has the record of its calls
+    ws = cache.attention_workspace(good, 4)
+    cache.attention(rows(counts, bad), q, ws=ws)
+    assert nv.read_device_error(cache.ws_rows) == (nv.OK, 0)
+    assert nv.read_device_error(ws) == (nv.ERR_DEVICE, 1)
+
+
+def test_a_captured_attention_without_a_workspace_reports_too():
+    require_gpu()
+    cache, rows, table = _step([1, 1], [40, 3000])
+    q = dev_bf16(syn.normal_bf16((2, 4, 64), seed=3))
+    r = rows([1, 1])
+    want = cache.attention(r, q).clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = cache.attention(r, q)
+    graph.replay()
+    assert nv.read_device_error(cache.ws_rows) == (nv.OK, 0) and torch.equal(out, want)
+    good = r.pages.clone()
+    r.pages[1, 3] = -5
+    graph.replay()
+    assert nv.read_device_error(cache.ws_rows) == (nv.ERR_DEVICE, 1)
+    r.pages.copy_(good)
+    graph.replay()
+    assert nv.read_device_error(cache.ws_rows) == (nv.OK, 0) and torch.equal(out, want)

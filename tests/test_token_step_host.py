@@ -27,3 +27,16 @@ def test_gemv_without_rows(L):
     assert call(ldx=192) == call(y=FAKE, ldy=95) == call(act=7) == nv.ERR_INVALID_ARG
     assert call(k=200) == call(out_codes=FAKE) == nv.ERR_UNSUPPORTED
     assert call(m=1, x=FAKE) == call(m=1, y=FAKE) == nv.ERR_INVALID_ARG
+
+
+def test_attention_with_a_record_of_its_own(L):
+    cache = nv.CPagedCache(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 8, 16, 2, 64)
+    rows = nv.CPagedRows(FAKE, FAKE, FAKE, 3, 4, 5, 2, 60)
+
+    def call(record=FAKE, ws=FAKE, n=1 << 30, heads=4, r=rows):
+        return L.nvfp4_paged_attention_recorded(ctypes.byref(cache), ctypes.byref(r), FAKE, 256, heads, 0, 0, 0.0, FAKE, 256,
+                                                ws, n, record, None)
+
+    assert call(record=None) == call(heads=3) == call(ws=None) == call(n=255) == nv.ERR_INVALID_ARG
+    assert call(record=FAKE + 16) == call(ws=FAKE + 16) == nv.ERR_MISALIGNED
+    assert call(r=nv.CPagedRows(FAKE, FAKE, FAKE, 0, 4, 5, 2, 60)) == nv.OK  # no sequences
