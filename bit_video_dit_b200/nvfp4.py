@@ -405,7 +405,8 @@ def gemv(x: torch.Tensor, w: NVFP4Tensor, *, out: torch.Tensor | None = None, ou
     elif out.dtype != torch.bfloat16 or out.shape != (M, N):
         raise ValueError("out is bf16 [M, N]")
     ldy, sy = out.stride()
-    if (sy != 1 and N > 1) or out.get_device() != index or w.codes.get_device() != index:
+    if ((sy != 1 and N > 1) or out.get_device() != index or w.codes.get_device() != index or
+            w.scales.get_device() != index or w.global_scale.get_device() != index):
         raise ValueError(f"x, the weight and out have to be on {x.device}, out with unit column stride")
     ep = None
     if act or not (bias is mod_scale is mod_shift is gate is residual is out_f32 is None):
@@ -604,6 +605,12 @@ class PagedKVCache:
             raise ValueError("the heads of a row have to be contiguous")
         return ld if rows.n_rows > 1 else heads * self.head_dim  # a row stride means nothing for a single row
 
+    def _memory(self, ws: torch.Tensor) -> tuple[int, int]:
+        """Address and bytes of a workspace."""
+        if ws.get_device() != self.index or not ws.is_contiguous():
+            raise ValueError(f"the workspace has to be contiguous memory on {self.device}")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+
     def append(self, rows: PagedRows, k: torch.Tensor, v: torch.Tensor, *, rope=None, ws: torch.Tensor | None = None,
                stream=None) -> None:
         """Quantize the rows' K and V (bf16 [n_rows, kv_heads, d], rows may be strided) into their pages.  rope =
@@ -619,7 +626,7 @@ class PagedKVCache:
                     raise ValueError(f"rope tables are contiguous float32 [n_rows, d / 2] on {self.device}")
         ws = self.ws_rows if ws is None else ws
         st = _launch_on(self.index, stream, lib().nvfp4_paged_append, self._ref, rows._ref, k.data_ptr(), ld_k,
-                        v.data_ptr(), ld_v, _ptr(cos), _ptr(sin), ws.data_ptr(), ws.numel())
+                        v.data_ptr(), ld_v, _ptr(cos), _ptr(sin), *self._memory(ws))
         if st:
             _check("nvfp4_paged_append", st)
 
@@ -636,7 +643,7 @@ class PagedKVCache:
         ld_k, ld_v = self._row_stride(rows, heads, k_out), self._row_stride(rows, heads, v_out)
         ws = self.ws_rows if ws is None else ws
         st = _launch_on(self.index, stream, lib().nvfp4_paged_gather, self._ref, rows._ref, k_out.data_ptr(), ld_k,
-                        v_out.data_ptr(), ld_v, ws.data_ptr(), ws.numel())
+                        v_out.data_ptr(), ld_v, *self._memory(ws))
         if st:
             _check("nvfp4_paged_gather", st)
         return k_out, v_out
@@ -668,7 +675,7 @@ class PagedKVCache:
                 ws = self._attention_memory(rows, heads, window, sinks)
         ld_q, ld_o = self._row_stride(rows, heads, q), self._row_stride(rows, heads, out)
         st = _launch_on(self.index, stream, lib().nvfp4_paged_attention_recorded, self._ref, rows._ref, q.data_ptr(), ld_q,
-                        heads, window, sinks, scale, out.data_ptr(), ld_o, ws.data_ptr(), ws.numel(), record.data_ptr())
+                        heads, window, sinks, scale, out.data_ptr(), ld_o, *self._memory(ws), record.data_ptr())
         if st:
             _check("nvfp4_paged_attention", st)
         return out

@@ -82,3 +82,34 @@ def test_a_captured_attention_without_a_workspace_reports_too():
     r.pages.copy_(good)
     graph.replay()
     assert nv.read_device_error(cache.ws_rows) == (nv.OK, 0) and torch.equal(out, want)
+
+
+def test_tensors_on_another_device_are_refused():
+    """Here the host: a weight's scales and workspaces."""
+    require_gpu()
+    w, x = _weight(), dev_bf16(syn.normal_bf16((4, 256), seed=2))
+    for part in ("codes", "scales", "global_scale"):
+        parts = {name: getattr(w, name) for name in ("codes", "scales", "global_scale")}
+        parts[part] = parts[part].cpu()
+        with pytest.raises(ValueError):
+            nv.gemv(x, nv.NVFP4Tensor(rows=w.rows, cols=w.cols, **parts))
+    cache, rows, _ = _step([1, 1], [40, 60])
+    r = rows([1, 1])
+    k, q = dev_bf16(syn.normal_bf16((2, 2, 64), seed=3)), dev_bf16(syn.normal_bf16((2, 4, 64), seed=3))
+    ws = cache.attention_workspace(r, 4)
+    for bad in (ws.cpu(), ws[:1].expand(1 << 20), torch.zeros(2 * ws.numel(), dtype=torch.uint8, device="cuda")[::2]):
+        for call in (lambda: cache.append(r, k, k, ws=bad), lambda: cache.gather(r, ws=bad),
+                     lambda: cache.attention(r, q, ws=bad)):
+            with pytest.raises(ValueError):
+                call()
+
+
+def test_a_workspace_of_words_counts_its_bytes():
+    require_gpu()
+    cache, rows, _ = _step([1, 1], [40, 3000])
+    r, q = rows([1, 1]), dev_bf16(syn.normal_bf16((2, 4, 64), seed=3))
+    ws = cache.attention_workspace(r, 4)
+    words = torch.zeros(ws.numel() // 4, dtype=torch.int32, device="cuda")
+    assert torch.equal(cache.attention(r, q, ws=words), cache.attention(r, q, ws=ws))
+    with pytest.raises(nv.NVFP4Error):
+        cache.attention(r, q, ws=words[:-1])
