@@ -384,6 +384,13 @@ def _same_device(device: torch.device, *ts) -> None:
             raise ValueError(f"every tensor of the call has to be on {device}")
 
 
+def _int32(**numbers) -> None:
+    """The C interface's integers are 32 bits wide, and ctypes drops the bits above them."""
+    for name, n in numbers.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise ValueError(f"{name} = {n} does not fit in 32 bits")
+
+
 def gemv(x: torch.Tensor, w: NVFP4Tensor, *, out: torch.Tensor | None = None, out_f32: torch.Tensor | None = None,
          bias=None, mod_scale=None, mod_shift=None, gate=None, residual=None, act: int = ACT_NONE,
          stream=None) -> torch.Tensor:
@@ -548,6 +555,7 @@ class PagedRows:
         if row_start.shape != (B + 1,) or lens.dim() != 1 or pages.dim() != 2 or pages.shape[0] != B:
             raise ValueError("row_start is [B + 1], lens [B], pages [B, max_pages]")
         _same_device(lens.device, row_start, pages)
+        _int32(n_rows=n_rows, max_rows=max_rows, max_len=max_len)
         self.row_start, self.lens, self.pages = row_start, lens, pages
         self.n_seqs, self.n_rows, self.max_rows, self.max_len = B, n_rows, max_rows, max_len
         self.index = lens.get_device()
@@ -649,6 +657,7 @@ class PagedKVCache:
         return k_out, v_out
 
     def _attention_memory(self, rows: PagedRows, heads: int, window: int, sinks: int) -> torch.Tensor:
+        _int32(heads=heads, window=window, sinks=sinks)
         n = int(lib().nvfp4_paged_attention_workspace_bytes(self._ref, rows._ref, heads, window, sinks))
         if n == 0:
             raise ValueError("nvfp4_paged_attention_workspace_bytes: refused arguments")
@@ -667,6 +676,7 @@ class PagedKVCache:
         if q.dim() != 3:
             raise ValueError("attention takes q [n_rows, heads, head_dim]")
         heads = q.shape[1]
+        _int32(window=window, sinks=sinks)
         record = self.ws_rows if ws is None else ws
         with _allocating_for(stream):
             if out is None:

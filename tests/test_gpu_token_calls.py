@@ -113,3 +113,21 @@ def test_a_workspace_of_words_counts_its_bytes():
     assert torch.equal(cache.attention(r, q, ws=words), cache.attention(r, q, ws=ws))
     with pytest.raises(nv.NVFP4Error):
         cache.attention(r, q, ws=words[:-1])
+
+
+def test_numbers_beyond_32_bits_are_refused():
+    """None of them may come out as its low bits (a window of 2^32 + 5 as one of 5)."""
+    require_gpu()
+    cache, rows, _ = _step([1, 1], [40, 60])
+    r, q = rows([1, 1]), dev_bf16(syn.normal_bf16((2, 4, 64), seed=3))
+    ws = cache.attention_workspace(r, 4)
+    for kw in (dict(window=2 ** 32 + 5), dict(window=30, sinks=2 ** 32), dict(window=2 ** 31)):
+        with pytest.raises(ValueError):
+            cache.attention(r, q, ws=ws, **kw)
+        with pytest.raises(ValueError):
+            cache.attention_workspace(r, 4, **kw)
+    with pytest.raises(ValueError):
+        cache.attention_workspace(r, 2 ** 32 + 4)
+    for kw in (dict(n_rows=2 ** 32 + 2), dict(max_rows=2 ** 32 + 1), dict(max_len=2 ** 32)):
+        with pytest.raises(ValueError):
+            nv.PagedRows(r.row_start, r.lens, r.pages, **{**dict(n_rows=2, max_rows=1, max_len=60), **kw})
