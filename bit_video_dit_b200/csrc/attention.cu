@@ -76,6 +76,18 @@ __host__ __device__ constexpr uint32_t idesc_f16(int b_mn, int bf) {
            ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 }
 
+// 16-bit MMA (kind::f16): D[tmem] (+)= A B, K = 16 per op, binary32 accumulation.
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // 8 E2M1 codes with their block scale and the slot's a32 -> 8 bf16, as the
 // cache's dequant: bf16_rne(fl32(fl32(e2m1 * s) * a32) [+ mean]).
 __device__ __forceinline__ uint4 dq8(uint32_t q, uint32_t sc, float a32, const float* m) {
