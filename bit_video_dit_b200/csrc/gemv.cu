@@ -27,8 +27,9 @@
 // through the ring before its pieces and have a power of their own, which comes
 // off the chunk's sums.
 //
-// Measured: 28672 x 8192 (132 MB) 31 us with one row (4.2 TB/s), 40 with 8, 49
-// with 16; 14336 x 4096 12.5, 14, 18.  What bounds it is the conversion and
+// Measured (here and below: no epilogue, calls in a graph, weights read from
+// DRAM): 28672 x 8192 (132 MB) 31 us with one row (4.2 TB/s), 40 with 8, 49
+// with 16; 14336 x 4096 12.4, 13.9, 17.7.  What bounds it is the conversion and
 // integer pipe, with the issue slots half full: decoding a pair of codes takes
 // 3.6 cycles of a scheduler, which alone is 14 us of that weight, and scaling the
 // activations, addresses and scale bytes the rest; hence few, large passes.
@@ -94,8 +95,15 @@ __device__ __forceinline__ uint4 lds16(uint32_t p) {
 
 // What a CTA computes: `whole` quads from quad0 on, then the groups [g0, g1) of
 // those that whole quads for every CTA leave over: one, an aligned pair or a
-// quad, so that they lie in one quad (a piece's overhead is per quad; dealt out
-// evenly, two groups of 4096 x 4096 lay in two: 8.1 us a product, 6.4 so).
+// quad, so that they lie in one quad (a piece's overhead is per quad).  Some CTAs
+// then have less than others, or nothing; but dealt out evenly a share often lies
+// in two quads.  One row, 16 rows (us; evenly):
+//   4096 x 4096    6.2,  9.5  (8.0, 12.0)    9216 x 4096    8.2, 11.8  (9.9, 13.9)
+//   5120 x 5120    8.5, 14.0 (10.3, 15.0)   14336 x 4096   12.4, 17.7 (13.3, 18.5)
+//   6144 x 4096    7.7, 11.8  (9.0, 13.0)   28672 x 8192   31.2, 49.2 (31.4, 50.2)
+// With 8 rows the wide ones lose by it: 20000 x 4096 17.1 (16.9), 28672 x 8192
+// 40.4 (39.2).  The longest share stays above the mean (2.3 times at 1024 rows, 1.3
+// at 14336): K is not split over CTAs.
 struct Share {
     int quad0, whole, g0, g1;
     __device__ __forceinline__ int count() const { return whole + (g1 > g0 ? 1 : 0); }

@@ -28,8 +28,9 @@ using namespace fp4mma;
 // the rows are aligned to that: 53 -> 37 us for 51k rows of 8 heads of 64 read
 // back).  Finding a row's place takes five dependent loads, so a warp takes
 // several heads of K and V of its rows, 4 (append, whose arithmetic needs the
-// registers) or 8 (gather) of them at a time.  2640 rows x 24 heads x 128:
-// append with RoPE 15.5 us (2.7 TB/s), gather 12 us (3.4 TB/s).
+// registers) or 8 (gather) of them at a time.  2640 rows x 24 heads x 128 (calls
+// in a graph, data from DRAM): append with RoPE 14.1 us (3.0 TB/s), gather 10.9
+// (3.8); the 51k rows 35.2 (4.8).
 // ---------------------------------------------------------------------------
 constexpr int kRowWarps = 8;
 
@@ -216,9 +217,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, 3) rows_kernel(const __grid_co
 //
 // Bound: the cache's bytes (a key and value are 9/8 head_dim bytes a head),
 // and beside them the decoding (fp4mma.cuh).  64 sequences of 6000 keys on
-// average x 8 heads of 128 (177 MB): 49 us, of which the runs' beginnings and
-// ends (places, pages, queries; joining) are 12; the copies alone then take 27
-// (6.5 TB/s), the arithmetic alone 31, both 37.
+// average x 8 heads of 128 (177 MB; calls in a graph): 47 us, of which the runs'
+// beginnings and ends (places, pages, queries; joining) are about 11; the copies
+// alone then take 27 (6.5 TB/s), the arithmetic alone 31, both 37.
 // ---------------------------------------------------------------------------
 constexpr int kKeys = 32;  // keys of a tile
 constexpr int kSms = 148;

@@ -19,15 +19,16 @@
 // * 16 + (c % 8) * 2: Q, K and P K-major, V MN-major.  TMEM: S_A[2], S_B[2] (64
 // columns each) and O_A, O_B.  Scores are double-buffered: QK(j + 2) is issued
 // as soon as the softmax has read S of tile j, so that it finds the next tile's
-// done.  2640 rows x 24 heads over 23760 visible keys: 737 us with one buffer of
-// 128 keys and one issuing thread, 706 so, 692 with rows read and written eight
-// lanes a line (990 TFLOP/s of what the rows see).
+// done.  One buffer of 128 keys and one issuing thread took 4% more, rows read and
+// written a lane a row another 2%.  2640 rows x 24 heads over 23760 visible keys:
+// 723 us in a graph that repeats one input (950 TFLOP/s of what the rows see), 730
+// with inputs in turn, 762 back to back from Python with inputs in turn.
 // What is left is no unit's rate (products 1280 cycles of a tile's 2300,
 // exponentials 1024, issue 45%) but the hand-overs between the roles: without
-// the softmax's and the producers' work the same barriers take 640 us.
-// Measured and not taken: 16 softmax warps (each half a tile's columns; 1024
-// us), four issuing threads (752), a lane waiting for its warp (820), an eighth
-// of the exponentials as polynomials (747).
+// the softmax's and the producers' work the same barriers take 0.93 of the time.
+// Measured and not taken (of the time of the day): 16 softmax warps (each half a
+// tile's columns; 1.48), four issuing threads (1.09), a lane waiting for its warp
+// (1.18), an eighth of the exponentials as polynomials (1.08).
 // The softmax takes one pass a tile against a reference 7 binary orders below the
 // largest score (paged.cuh) that moves only when a row's weights in the tile sum
 // above 2^15 (binary16 holds those below).  Every wait is bounded; a timeout records NVFP4_ERR_TIMEOUT and every

@@ -279,8 +279,8 @@ nvfp4_status nvfp4_gemm(const nvfp4_tensor* A, const nvfp4_tensor* B, void* c_bf
  * Products of binary16 operands: e2m1 * s is exact there; a row of x is scaled
  * by a power of two (a row whose activations do not fit in shared memory: each
  * 128 columns by their own), which rounds only values below 2^-28 of the largest
- * of them.  Binary32 sums in a fixed order.  A NaN stays in its row.  One
- * launch, no workspace. */
+ * of them.  Binary32 sums in a fixed order.  A NaN stays in its row.  y must not
+ * overlap x (it may be the residual).  One launch, no workspace. */
 nvfp4_status nvfp4_gemv(const void* x_bf16, int64_t m, int64_t ldx, const nvfp4_tensor* W, void* y_bf16, int64_t ldy,
                         const nvfp4_epilogue* ep, nvfp4_stream_t stream);
 
@@ -398,8 +398,8 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const int32_t* slot
 /* The slots above hold whole frame-chunks under the chunk's own tensor scale.
  * Here a sequence grows by any number of tokens a step, so each of K and V has
  * one tensor scale for the whole cache, given by the caller (as
- * NVFP4_Q_GIVEN_GLOBAL: amax / 2688 of a calibration; larger values saturate),
- * and the block scales follow each token.
+ * NVFP4_Q_GIVEN_GLOBAL: amax / 2688 of a calibration, never negative; larger
+ * values saturate), and the block scales follow each token.
  * Row (p * kv_heads + h) * page_size + o is token o of page p, head h: its
  * head_dim / 2 code bytes at that multiple in *_codes, its head_dim / 16 scale
  * bytes in *_scales.  head_dim 64 or 128, page_size a multiple of 16 up to
@@ -471,7 +471,9 @@ nvfp4_status nvfp4_paged_gather(const nvfp4_paged_cache* cache, const nvfp4_page
  * binary16 (2^-11 of each, and 2^-32 of the row's largest for those below 2^-21
  * of it).  A row that sees no key gives zeros.  Pages that hold no visible
  * key are not looked up, so a window's caller may have given them back; places
- * that no row sees may hold any bytes.  A NaN query gives NaN, in its row alone.
+ * that no row sees may hold any bytes (what an append writes is always finite; a
+ * NaN scale put by other means where some row sees it may reach rows of the call
+ * that do not).  A NaN query gives NaN, in its row alone.
  * workspace: nvfp4_paged_attention_workspace_bytes of the same arguments (0:
  * refused; at most 40 MB); results do not depend on what it
  * holds behind the control block.  Up to 16 (row, query head) pairs a K/V head
