@@ -26,13 +26,13 @@
 // What is left is no unit's rate (products 1280 cycles of a tile's 2300,
 // exponentials 1024, issue 45%) but the hand-overs between the roles: without
 // the softmax's and the producers' work the same barriers take 0.93 of the time.
-// Measured and not taken (of the time of the day): 16 softmax warps (each half a
-// tile's columns; 1.48), four issuing threads (1.09), a lane waiting for its warp
-// (1.18), an eighth of the exponentials as polynomials (1.08).
+// Measured and not taken (times against the kernel then): 16 softmax warps (each
+// half a tile's columns; 1.48), four issuing threads (1.09), a lane waiting for its
+// warp (1.18), an eighth of the exponentials as polynomials (1.08).
 // The softmax takes one pass a tile against a reference 7 binary orders below the
 // largest score (paged.cuh) that moves only when a row's weights in the tile sum
-// above 2^15 (binary16 holds those below).  Every wait is bounded; a timeout records NVFP4_ERR_TIMEOUT and every
-// role stops.
+// above 2^15 (binary16 holds those below).  Every wait is bounded; a timeout
+// records NVFP4_ERR_TIMEOUT and every role stops.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
